@@ -37,6 +37,12 @@ class _LayerStruct(ctypes.Structure):
     ]
 
 
+class _MlpStruct(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("I", ctypes.c_int), ("gate_up", ctypes.c_void_p),
+                ("ld_gate_up", ctypes.c_longlong), ("gate_up_scale", ctypes.c_void_p), ("down", ctypes.c_void_p),
+                ("ld_down", ctypes.c_longlong), ("down_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -90,6 +96,24 @@ def lib():
         L.moe_q4_lloyd_hist.argtypes = [vp, ctypes.c_longlong, vp, ci, vp, sz, vp]
         L.moe_q4_lloyd_solve.argtypes = [vp, ci, ctypes.c_double, vp, vp, vp, sz, vp]
         L.moe_q4_forward_host_async.argtypes = L.moe_q4_forward_host.argtypes
+        ll, mlp = ctypes.c_longlong, ctypes.POINTER(_MlpStruct)
+        L.moe_q4_quant_rows.argtypes = [vp, ci, ll, ci, ci, vp, ll, vp, vp]
+        L.moe_q4_add_norm.argtypes = [vp, ci, ll, vp, ci, ll, vp, ll, vp, ci, ctypes.c_float, ci, ci, vp, ll, vp, ll,
+                                      vp, vp]
+        L.moe_q4_linear_i8.argtypes = [vp, ll, vp, vp, ll, vp, vp, ci, ci, ci, vp, ci, ll, vp]
+        L.moe_q4_mlp_i8_workspace.argtypes = [mlp, ci]
+        L.moe_q4_mlp_i8.argtypes = [mlp, vp, ll, vp, ci, vp, ci, ll, vp, sz, vp]
+        layer = ctypes.POINTER(_LayerStruct)
+        L.moe_q4_forward_ex_i8_workspace.argtypes = [layer, mlp, ci, ci]
+        L.moe_q4_forward_ex_i8.argtypes = [layer, mlp, vp, vp, ll, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_q4_forward_gated_i8_workspace.argtypes = [layer, mlp, ci, ci]
+        L.moe_q4_forward_gated_i8.argtypes = [layer, mlp, vp, vp, vp, ll, vp, ci, ci, vp, vp, vp, vp, vp, vp, vp, sz,
+                                              vp]
+        for f in (L.moe_q4_mlp_i8_workspace, L.moe_q4_forward_ex_i8_workspace, L.moe_q4_forward_gated_i8_workspace):
+            f.restype = sz
+        for f in (L.moe_q4_quant_rows, L.moe_q4_add_norm, L.moe_q4_linear_i8, L.moe_q4_mlp_i8,
+                  L.moe_q4_forward_ex_i8, L.moe_q4_forward_gated_i8):
+            f.restype = ci
         for f in (L.moe_q4_pack, L.moe_q4_dequant, L.moe_q4_forward, L.moe_q4_forward_host,
                   L.moe_q4_forward_host_async,
                   L.moe_q4_forward_status, L.moe_q4_read_status, L.moe_q4_route,
@@ -256,20 +280,34 @@ class Shared:
 
 
 def forward_ex_workspace(layer: Layer, shared, T: int, k: int) -> int:
+    if isinstance(shared, MlpI8):
+        return int(lib().moe_q4_forward_ex_i8_workspace(ctypes.byref(layer.struct()), shared.ref, T, k))
     sh = ctypes.byref(shared.struct()) if shared is not None else None
     return int(lib().moe_q4_forward_ex_workspace(ctypes.byref(layer.struct()), sh, T, k))
 
 
 def forward_ex(layer: Layer, shared, x: torch.Tensor, logits: torch.Tensor, k: int, out=None, ws=None,
-               topk_ids=None, topk_w=None, counts=None, out_f32=None, stream=None) -> torch.Tensor:
-    """One MoE layer with a shared expert (shared may be None)."""
+               topk_ids=None, topk_w=None, counts=None, out_f32=None, stream=None, xq=None,
+               x_scale=None) -> torch.Tensor:
+    """One MoE layer with a shared expert: a Shared (bf16), an MlpI8 (int8;
+    xq and x_scale are x's int8 rows where the caller has them, as add_norm
+    gives them, else the call makes them) or None."""
     T = x.shape[0]
+    ldq = _shared_rows(layer, shared, xq, x_scale, T)
     if out is None:
         out = torch.empty((T, layer.H), dtype=torch.bfloat16, device=x.device)
     own_ws = ws is None
     if own_ws:
         ws = alloc_workspace(forward_ex_workspace(layer, shared, T, k), x.device)
     st = layer.struct()
+    if isinstance(shared, MlpI8):
+        _check(lib().moe_q4_forward_ex_i8(ctypes.byref(st), shared.ref, _ptr(x), _ptr(xq), ldq, _ptr(x_scale),
+                                          _ptr(logits), T, k, _ptr(out), _ptr(out_f32), _ptr(topk_ids), _ptr(topk_w),
+                                          _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)),
+               "moe_q4_forward_ex_i8")
+        if own_ws:
+            _hold(stream, ws)
+        return out
     ss = shared.struct() if shared is not None else None
     _check(lib().moe_q4_forward_ex(ctypes.byref(st), ctypes.byref(ss) if ss is not None else None, _ptr(x),
                                    _ptr(logits), T, k, _ptr(out), _ptr(out_f32), _ptr(topk_ids), _ptr(topk_w),
@@ -280,24 +318,36 @@ def forward_ex(layer: Layer, shared, x: torch.Tensor, logits: torch.Tensor, k: i
 
 
 def forward_gated_workspace(layer: Layer, shared, T: int, k: int) -> int:
+    if isinstance(shared, MlpI8):
+        return int(lib().moe_q4_forward_gated_i8_workspace(ctypes.byref(layer.struct()), shared.ref, T, k))
     sh = ctypes.byref(shared.struct()) if shared is not None else None
     return int(lib().moe_q4_forward_gated_workspace(ctypes.byref(layer.struct()), sh, T, k))
 
 
 def forward_gated(layer: Layer, shared, router_w: torch.Tensor, x: torch.Tensor, k: int, out=None, ws=None,
-                  logits=None, topk_ids=None, topk_w=None, counts=None, out_f32=None, stream=None) -> torch.Tensor:
+                  logits=None, topk_ids=None, topk_w=None, counts=None, out_f32=None, stream=None, xq=None,
+                  x_scale=None) -> torch.Tensor:
     """One MoE layer from the hidden states: the bf16 router gate router_w
     [E, H] computes the logits (into `logits` [T, E] fp32 when given), then
-    the layer as forward_ex (shared may be None)."""
+    the layer as forward_ex (shared, xq and x_scale as there)."""
     if router_w.dtype != torch.bfloat16 or tuple(router_w.shape) != (layer.E, layer.H):
         raise ValueError(f"router_w must be bf16 [{layer.E}, {layer.H}]")
     T = x.shape[0]
+    ldq = _shared_rows(layer, shared, xq, x_scale, T)
     if out is None:
         out = torch.empty((T, layer.H), dtype=torch.bfloat16, device=x.device)
     own_ws = ws is None
     if own_ws:
         ws = alloc_workspace(forward_gated_workspace(layer, shared, T, k), x.device)
     st = layer.struct()
+    if isinstance(shared, MlpI8):
+        _check(lib().moe_q4_forward_gated_i8(ctypes.byref(st), shared.ref, _ptr(router_w), _ptr(x), _ptr(xq), ldq,
+                                             _ptr(x_scale), T, k, _ptr(out), _ptr(out_f32), _ptr(logits),
+                                             _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(ws), ws.numel(),
+                                             _stream(stream)), "moe_q4_forward_gated_i8")
+        if own_ws:
+            _hold(stream, ws)
+        return out
     ss = shared.struct() if shared is not None else None
     _check(lib().moe_q4_forward_gated(ctypes.byref(st), ctypes.byref(ss) if ss is not None else None,
                                       _ptr(router_w), _ptr(x), T, k, _ptr(out), _ptr(out_f32), _ptr(logits),
@@ -431,3 +481,209 @@ def combine(y: torch.Tensor, w: torch.Tensor, inv=None, out=None, out_f32=None, 
            "moe_q4_combine")
     _hold(stream, y, w)
     return out
+
+
+# ---- 8-bit integer rows, products and the int8 MLP -------------------------
+
+_ROW_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _row_stride(t, what, dtypes=_ROW_TYPE, cols=None, rows=None, pad=1):
+    """Check a CUDA matrix of consecutive elements in each row; its row stride
+    in elements (that of a single row is of no consequence)."""
+    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA matrix of {' or '.join(str(d) for d in dtypes)}")
+    n, k = t.shape
+    if (cols is not None and k != cols) or (rows is not None and n != rows):
+        raise ValueError(f"{what} must be [{n if rows is None else rows}, {k if cols is None else cols}], "
+                         f"not [{n}, {k}]")
+    ld, inner = t.stride()
+    if inner != 1 and k > 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+    if n > 1:
+        return ld
+    return -(-k // pad) * pad
+
+
+def _vector(t, what, n, dtypes=(torch.float32,)):
+    if t.dim() != 1 or t.dtype not in dtypes or not t.is_cuda or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA vector of {n} {' or '.join(str(d) for d in dtypes)}")
+    return t.data_ptr()
+
+
+class _On:
+    """The device of a call's tensors as the current one, and the stream's handle."""
+
+    def __init__(self, stream, first, *others):
+        dev = first.device
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError("the tensors of a call must be on one device")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError("the stream must be of the tensors' device")
+        self.handle = stream.cuda_stream
+        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _codes(T, K, device):
+    """An int8 [T, K] whose rows start on 16 bytes, as the products read them."""
+    return torch.empty((T, -(-K // 16) * 16), dtype=torch.int8, device=device)[:, :K]
+
+
+def quant_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """bf16 or fp32 rows x [T, K] -> (codes int8 [T, K], scales fp32 [T]): for
+    each row scale = max|x| / 127 and the codes nearest to 127 x / max|x|, ties
+    to even.  A new q has rows on 16-byte boundaries (linear_i8's operands)."""
+    ldx = _row_stride(x, "x")
+    T, K = x.shape
+    new = q is None, scale is None
+    if new[0]:
+        q = _codes(T, K, x.device)
+    if new[1]:
+        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    ldq = _row_stride(q, "q", (torch.int8,), K, T)
+    sp = _vector(scale, "scale", T)
+    with _On(stream, x, q, scale) as h:
+        _check(lib().moe_q4_quant_rows(x.data_ptr(), _ROW_TYPE[x.dtype], ldx, T, K, q.data_ptr(), ldq, sp, h),
+               "moe_q4_quant_rows")
+    _hold(stream, q if new[0] else None, scale if new[1] else None)
+    return q, scale
+
+
+def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             q: torch.Tensor | None = None, scale: torch.Tensor | None = None, bf16: bool = True,
+             quant: bool = True, stream=None):
+    """Residual addition, root-mean-square norm and the norm's rows in bf16 and
+    int8 in one pass: r = x + residual (in the residual's type), then
+    r * weight / sqrt(mean(r^2) + eps).  x and residual bf16 or fp32 [T, H],
+    weight bf16 or fp32 [H] or None (ones).  Returns (r or None without a
+    residual, out bf16 [T, H] or None with bf16=False, codes int8 [T, H] and
+    scales fp32 [T] or None with quant=False).  residual_out may be residual
+    itself (in place), out may be a bf16 x."""
+    ldx = _row_stride(x, "x")
+    T, H = x.shape
+    dev = x.device
+    made = []
+
+    def own(t):
+        made.append(t)
+        return t
+
+    ldr = ldro = ldo = ldq = rt = wt = 0
+    rp = rop = wp = op = qp = sp = None
+    if residual is not None:
+        ldr, rt, rp = _row_stride(residual, "residual", cols=H, rows=T), _ROW_TYPE[residual.dtype], residual.data_ptr()
+        if residual_out is None:
+            residual_out = own(torch.empty((T, H), dtype=residual.dtype, device=dev))
+        ldro, rop = _row_stride(residual_out, "residual_out", (residual.dtype,), H, T), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if weight is not None:
+        wp, wt = _vector(weight, "weight", H, _ROW_TYPE), _ROW_TYPE[weight.dtype]
+    if bf16 or out is not None:
+        if out is None:
+            out = own(torch.empty((T, H), dtype=torch.bfloat16, device=dev))
+        ldo, op = _row_stride(out, "out", (torch.bfloat16,), H, T), out.data_ptr()
+    if quant or q is not None or scale is not None:
+        if q is None:
+            q = own(_codes(T, H, dev))
+        if scale is None:
+            scale = own(torch.empty(T, dtype=torch.float32, device=dev))
+        ldq, qp, sp = _row_stride(q, "q", (torch.int8,), H, T), q.data_ptr(), _vector(scale, "scale", T)
+    with _On(stream, x, residual, residual_out, weight, out, q, scale) as h:
+        _check(lib().moe_q4_add_norm(x.data_ptr(), _ROW_TYPE[x.dtype], ldx, rp, rt, ldr, rop, ldro, wp, wt,
+                                     eps, T, H, op, ldo, qp, ldq, sp, h), "moe_q4_add_norm")
+    _hold(stream, *made)
+    return residual_out, out, q, scale
+
+
+def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Int8 rows x [T, K] with scales x_scale [T] times int8 weights w [N, K]
+    with scales w_scale [N], sums exact in int32: out [T, N] in bf16 or fp32
+    (dtype, or out's), plus an fp32 bias [N].  The rows of x and w start on
+    16-byte boundaries (quant_rows makes them so)."""
+    ldx = _row_stride(x, "x", (torch.int8,), pad=16)
+    T, K = x.shape
+    ldw = _row_stride(w, "w", (torch.int8,), cols=K, pad=16)
+    N = w.shape[0]
+    own = out is None
+    if own:
+        out = torch.empty((T, N), dtype=dtype, device=x.device)
+    ldo = _row_stride(out, "out", _ROW_TYPE, N, T)
+    with _On(stream, x, x_scale, w, w_scale, bias, out) as h:
+        _check(lib().moe_q4_linear_i8(x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), w.data_ptr(), ldw,
+                                      _vector(w_scale, "w_scale", N),
+                                      None if bias is None else _vector(bias, "bias", N), T, N, K, out.data_ptr(),
+                                      _ROW_TYPE[out.dtype], ldo, h), "moe_q4_linear_i8")
+    _hold(stream, out if own else None)
+    return out
+
+
+class MlpI8:
+    """A SwiGLU MLP with int8 weights: gate_up int8 [2I, H] (gate rows first)
+    with scales [2I], down int8 [H, I] with scales [H], as quant_rows makes
+    them of the bf16 matrices.  Also a layer's shared expert (forward_ex,
+    forward_gated)."""
+
+    def __init__(self, gate_up: torch.Tensor, gate_up_scale: torch.Tensor, down: torch.Tensor,
+                 down_scale: torch.Tensor):
+        ldg = _row_stride(gate_up, "gate_up", (torch.int8,), pad=16)
+        if gate_up.shape[0] % 2:
+            raise ValueError("gate_up holds the gate's rows and as many rows of the up projection")
+        self.I, self.H = gate_up.shape[0] // 2, gate_up.shape[1]
+        ldd = _row_stride(down, "down", (torch.int8,), self.I, self.H, pad=16)
+        gp, dp = _vector(gate_up_scale, "gate_up_scale", 2 * self.I), _vector(down_scale, "down_scale", self.H)
+        if len({t.device for t in (gate_up, gate_up_scale, down, down_scale)}) != 1:
+            raise ValueError("the tensors of an MLP must be on one device")
+        self.tensors = gate_up, gate_up_scale, down, down_scale
+        self.struct = _MlpStruct(self.H, self.I, gate_up.data_ptr(), ldg, gp, down.data_ptr(), ldd, dp)
+        self.ref = ctypes.byref(self.struct)
+
+
+def mlp_i8_workspace(mlp: MlpI8, T: int) -> int:
+    return int(lib().moe_q4_mlp_i8_workspace(mlp.ref, T))
+
+
+def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor | None = None,
+           dtype: torch.dtype = torch.bfloat16, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The int8 SwiGLU MLP: int8 rows x [T, H] with scales x_scale [T] -> out
+    [T, H] in bf16 or fp32 (dtype, or out's)."""
+    ldx = _row_stride(x, "x", (torch.int8,), mlp.H, pad=16)
+    T = x.shape[0]
+    own, own_ws = out is None, ws is None
+    if own:
+        out = torch.empty((T, mlp.H), dtype=dtype, device=x.device)
+    if own_ws:
+        ws = alloc_workspace(mlp_i8_workspace(mlp, T), x.device)
+    ldo = _row_stride(out, "out", _ROW_TYPE, mlp.H, T)
+    with _On(stream, x, x_scale, out, ws, mlp.tensors[0]) as h:
+        _check(lib().moe_q4_mlp_i8(mlp.ref, x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), T, out.data_ptr(),
+                                   _ROW_TYPE[out.dtype], ldo, ws.data_ptr(), ws.numel(), h), "moe_q4_mlp_i8")
+    _hold(stream, out if own else None, ws if own_ws else None)
+    return out
+
+
+def _shared_rows(layer, shared, xq, x_scale, T):
+    """Row stride of the int8 rows given to a forward beside x (0 for none)."""
+    if (xq is None) != (x_scale is None):
+        raise ValueError("xq and x_scale go together")
+    if xq is None:
+        return 0
+    if not isinstance(shared, MlpI8):
+        raise ValueError("xq and x_scale are read by an int8 shared expert (MlpI8)")
+    _vector(x_scale, "x_scale", T)
+    return _row_stride(xq, "xq", (torch.int8,), layer.H, T, pad=16)

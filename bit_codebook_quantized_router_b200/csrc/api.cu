@@ -65,12 +65,14 @@ bool shape_ok(const moe_q4_layer* L, int T, int top_k) {
 //   expert order, T > 16 only) | split-tile counters int32[units] | partial sums of the
 //   small-M kernels f32[2*160][4][min(16,T)][128] (two 128-row tiles per unit,
 //   gate/up then down) | with a shared expert: h_s | y_s | its split partial
-//   sums | with the router gate in front: logits f32[T][E] | its partial sums
+//   sums | with an int8 shared MLP: y_s | xq int8[T][H] | its scales f32[T] |
+//   the MLP's workspace | with the router gate in front: logits f32[T][E] |
+//   its partial sums
 struct Layout {
   size_t hdr, ids, w, counts, offsets, row_token, inv, dec_list, pre_list, mid_list, tiles, chunk_cnt,
       chunk_base, h, h_lo, y, xg,
       dk_counter,
-      dk_partial, h_s, y_s, sx_partial, logits, router_partial, end;
+      dk_partial, h_s, y_s, sx_partial, xq, xq_scale, mlp_ws, logits, router_partial, end;
   int dk_units_gu, dk_units_dn, n_max;
 };
 
@@ -81,7 +83,21 @@ bool shared_ok(const moe_q4_layer* L, const moe_q4_shared* S) {
   return L->H % 64 == 0;
 }
 
-Layout layout(const moe_q4_layer* L, int T, int k, const moe_q4_shared* S = nullptr, bool gated = false) {
+// An int8 shared MLP and the rows it reads: codes and scales of x, or null to
+// have the forward make them.
+struct SharedI8 {
+  const moe_q4_mlp* mlp;
+  const int8_t* xq;
+  long long ldxq;
+  const float* xq_scale;
+};
+
+bool mlp_ok(const moe_q4_layer* L, const moe_q4_mlp* M) {
+  return M && M->H == L->H && moe_q4_mlp_i8_workspace(M, 1) != 0;
+}
+
+Layout layout(const moe_q4_layer* L, int T, int k, const moe_q4_shared* S = nullptr, bool gated = false,
+              const moe_q4_mlp* M = nullptr) {
   const size_t R = (size_t)T * k;
   Layout o;
   size_t p = 0;
@@ -143,6 +159,17 @@ Layout layout(const moe_q4_layer* L, int T, int k, const moe_q4_shared* S = null
     o.sx_partial = p;
     p = align_up(p + (pa > pb ? pa : pb));
   }
+  o.xq = o.xq_scale = o.mlp_ws = 0;
+  if (M) {
+    o.y_s = p;
+    p = align_up(p + sizeof(float) * (size_t)T * L->H);
+    o.xq = p;
+    p = align_up(p + (size_t)T * L->H);
+    o.xq_scale = p;
+    p = align_up(p + sizeof(float) * (size_t)T);
+    o.mlp_ws = p;
+    p = align_up(p + moe_q4_mlp_i8_workspace(M, T));
+  }
   // router gate in front (moe_q4_forward_gated): logits f32 [T][E] | its partial sums
   o.logits = o.router_partial = 0;
   if (gated) {
@@ -176,8 +203,8 @@ HostStage host_stage(const moe_q4_layer* L, int T, size_t base) {
 int run_forward(const moe_q4_layer* L, const TableParams& tp, const void* x, const float* logits,
                 int T, int k, void* out, float* out_f32, int32_t* topk_ids, float* topk_w,
                 int32_t* counts, char* ws, cudaStream_t s, void* const* events = nullptr,
-                const moe_q4_shared* S = nullptr, const void* router_w = nullptr) {
-  const Layout o = layout(L, T, k, S, router_w != nullptr);
+                const moe_q4_shared* S = nullptr, const void* router_w = nullptr, const SharedI8* S8 = nullptr) {
+  const Layout o = layout(L, T, k, S, router_w != nullptr, S8 ? S8->mlp : nullptr);
   FwdArgs a;
   memset(&a, 0, sizeof a);
   a.T = T;
@@ -214,7 +241,7 @@ int run_forward(const moe_q4_layer* L, const TableParams& tp, const void* x, con
   a.h_lo = (__nv_bfloat16*)(ws + o.h_lo);
   a.y = (float*)(ws + o.y);
   a.out_f32 = out_f32;
-  a.y_s = S ? (const float*)(ws + o.y_s) : nullptr;
+  a.y_s = S || S8 ? (const float*)(ws + o.y_s) : nullptr;
   a.user_ids = topk_ids;
   a.user_w = topk_w;
   a.user_counts = counts;
@@ -277,6 +304,22 @@ int run_forward(const moe_q4_layer* L, const TableParams& tp, const void* x, con
     rc = q4_launch_dense(S->gate_up, 2, S->I, S->I, L->H, x, T, h_s, nullptr, S->I, part, a.hdr + kStatus, s);
     if (rc == MOE_Q4_OK)
       rc = q4_launch_dense(S->down, 1, 0, L->H, S->I, h_s, T, nullptr, y_s, L->H, part, a.hdr + kStatus, s);
+  }
+  if (rc == MOE_Q4_OK && S8) {
+    // the int8 shared MLP, on the caller's rows or on x brought to int8 here
+    const int8_t* xq = S8->xq;
+    const float* xs = S8->xq_scale;
+    long long ldxq = S8->ldxq;
+    if (!xq) {
+      int8_t* q = (int8_t*)(ws + o.xq);
+      rc = moe_q4_quant_rows(x, MOE_Q4_BF16, L->H, T, L->H, q, L->H, (float*)(ws + o.xq_scale), s);
+      xq = q;
+      xs = (const float*)(ws + o.xq_scale);
+      ldxq = L->H;
+    }
+    if (rc == MOE_Q4_OK)
+      rc = moe_q4_mlp_i8(S8->mlp, xq, ldxq, xs, T, ws + o.y_s, MOE_Q4_F32, L->H, ws + o.mlp_ws,
+                         moe_q4_mlp_i8_workspace(S8->mlp, T), s);
   }
   if (rc == MOE_Q4_OK) rc = mark(6);
   if (rc == MOE_Q4_OK) rc = q4_launch_combine(a, s);
@@ -400,6 +443,63 @@ extern "C" int moe_q4_forward_gated(const moe_q4_layer* layer, const moe_q4_shar
   float* lg = logits ? logits : reinterpret_cast<float*>((char*)ws + o.logits);
   return run_forward(layer, tp, x, lg, T, top_k, out, out_f32, topk_ids, topk_w, counts, (char*)ws,
                      (cudaStream_t)stream, nullptr, shared, router_w);
+}
+
+// The caller's int8 rows of x, where it has them: both pointers or neither.
+static bool rows_i8_ok(const moe_q4_layer* L, const int8_t* xq, long long ldxq, const float* x_scale) {
+  if (!xq && !x_scale) return true;
+  return xq && x_scale && !((uintptr_t)xq & 15) && !((uintptr_t)x_scale & 3) && ldxq >= L->H && ldxq % 16 == 0;
+}
+
+extern "C" size_t moe_q4_forward_ex_i8_workspace(const moe_q4_layer* layer, const moe_q4_mlp* shared, int T,
+                                                 int top_k) {
+  if (!shape_ok(layer, T, top_k) || !mlp_ok(layer, shared)) return 0;
+  return layout(layer, T, top_k, nullptr, false, shared).end;
+}
+
+extern "C" int moe_q4_forward_ex_i8(const moe_q4_layer* layer, const moe_q4_mlp* shared, const void* x,
+                                    const int8_t* xq, long long ldxq, const float* x_scale, const float* logits,
+                                    int T, int top_k, void* out, float* out_f32, int32_t* topk_ids, float* topk_w,
+                                    int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
+  if (!shape_ok(layer, T, top_k) || !mlp_ok(layer, shared)) return MOE_Q4_EINVAL;
+  TableParams tp;
+  int rc = q4_fill_tables(&tp, layer->tables, layer->n_tables, layer->table_id, layer->E);
+  if (rc != MOE_Q4_OK) return rc;
+  if (T == 0) return MOE_Q4_OK;
+  if (!x || !logits || !out || ((uintptr_t)x & 15) || ((uintptr_t)out & 15) || ((uintptr_t)logits & 3) ||
+      ((uintptr_t)out_f32 & 15) || !rows_i8_ok(layer, xq, ldxq, x_scale))
+    return MOE_Q4_EINVAL;
+  if (!ws || ((uintptr_t)ws & (kAlign - 1)) || ws_bytes < layout(layer, T, top_k, nullptr, false, shared).end)
+    return MOE_Q4_EWORKSPACE;
+  const SharedI8 s8 = {shared, xq, ldxq, x_scale};
+  return run_forward(layer, tp, x, logits, T, top_k, out, out_f32, topk_ids, topk_w, counts, (char*)ws,
+                     (cudaStream_t)stream, nullptr, nullptr, nullptr, &s8);
+}
+
+extern "C" size_t moe_q4_forward_gated_i8_workspace(const moe_q4_layer* layer, const moe_q4_mlp* shared, int T,
+                                                    int top_k) {
+  if (!shape_ok(layer, T, top_k) || !mlp_ok(layer, shared)) return 0;
+  return layout(layer, T, top_k, nullptr, true, shared).end;
+}
+
+extern "C" int moe_q4_forward_gated_i8(const moe_q4_layer* layer, const moe_q4_mlp* shared, const void* router_w,
+                                       const void* x, const int8_t* xq, long long ldxq, const float* x_scale, int T,
+                                       int top_k, void* out, float* out_f32, float* logits, int32_t* topk_ids,
+                                       float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
+  if (!shape_ok(layer, T, top_k) || !mlp_ok(layer, shared)) return MOE_Q4_EINVAL;
+  TableParams tp;
+  int rc = q4_fill_tables(&tp, layer->tables, layer->n_tables, layer->table_id, layer->E);
+  if (rc != MOE_Q4_OK) return rc;
+  if (T == 0) return MOE_Q4_OK;
+  if (!router_w || !x || !out || ((uintptr_t)router_w & 15) || ((uintptr_t)x & 15) || ((uintptr_t)out & 15) ||
+      ((uintptr_t)out_f32 & 15) || ((uintptr_t)logits & 3) || !rows_i8_ok(layer, xq, ldxq, x_scale))
+    return MOE_Q4_EINVAL;
+  const Layout o = layout(layer, T, top_k, nullptr, true, shared);
+  if (!ws || ((uintptr_t)ws & (kAlign - 1)) || ws_bytes < o.end) return MOE_Q4_EWORKSPACE;
+  float* lg = logits ? logits : reinterpret_cast<float*>((char*)ws + o.logits);
+  const SharedI8 s8 = {shared, xq, ldxq, x_scale};
+  return run_forward(layer, tp, x, lg, T, top_k, out, out_f32, topk_ids, topk_w, counts, (char*)ws,
+                     (cudaStream_t)stream, nullptr, nullptr, router_w, &s8);
 }
 
 extern "C" int moe_q4_forward_stages(const moe_q4_layer* layer, const void* x, const float* logits,

@@ -424,6 +424,128 @@ MOE_Q4_API int moe_q4_combine(const float* y, const float* w, const int32_t* inv
                               float* out_f32, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit integer rows.  A row v of K values is held as int8 codes in
+ * [-127, 127] and one fp32 scale:
+ *   scale = max|v| / 127;   code_i = the whole number nearest to
+ *   127 v_i / max|v|, a tie to the even one, of the exact quotient;
+ * v_i is then about code_i * scale.  A row of zeros has scale 0 and codes 0.
+ * A row that holds a NaN or an infinity has scale NaN and codes 0, so that
+ * every product with it is NaN (there is no status word).  Rows of
+ * activations have a scale for each token, rows of a weight matrix [N][K] one
+ * for each output channel.
+ *
+ * Matrices of these calls have a row stride in elements (ld...), at least the
+ * row's length, and consecutive elements in a row; int8 operands of products
+ * start on 16 bytes and have row strides that are multiples of 16 (bytes past
+ * a row's end are neither read nor written).  Element types of the others:
+ * ------------------------------------------------------------------------- */
+#define MOE_Q4_BF16 0
+#define MOE_Q4_F32 1
+
+/* moe_q4_quant_rows -- T rows to codes and scales.
+ *   x      device, bf16 or fp32 (x_type) [T][ldx];
+ *   T >= 0; K >= 1;
+ *   q      device int8 [T][ldq] (out);  scale  device fp32 [T] (out).
+ * The codes are exact as defined above; scale is one fp32 division.
+ * Alignment of x and q is that of their elements; 16-byte (x) and 8-byte (q)
+ * bases and row strides take the faster vector path.  No workspace. */
+MOE_Q4_API int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T, int K, int8_t* q, long long ldq,
+                                 float* scale, void* stream);
+
+/* moe_q4_add_norm -- the residual's addition, the root-mean-square norm and
+ * the norm's rows in bf16 and in int8, in one pass:
+ *   r = x + residual, rounded to the residual's type  (r = x without one);
+ *   p = r * weight  (fp32);   f = 1 / sqrt(mean(r^2) + eps)  (fp32);
+ *   residual_out = r;   out = bf16(p f);
+ *   codes of the row p;   scale = max|p| f / 127.
+ * The factor f is common to a row, so its codes are those of p: exact, and
+ * independent of the order in which the squares are summed.
+ *   x             device, bf16 or fp32 (x_type) [T][ldx];
+ *   residual      optional device, bf16 or fp32 (residual_type) [T][ldr], and
+ *   residual_out  device, the same type, [T][ldro] (out): both or neither;
+ *                 residual_out may be residual, or x where type and stride
+ *                 are the same;
+ *   weight        optional device, bf16 or fp32 (weight_type) [H], NULL: ones;
+ *   eps           > 0, finite;  T >= 0; H >= 1;
+ *   out           optional device bf16 [T][ldo] (out); may be a bf16 x of the
+ *                 same stride, not residual_out;
+ *   q, scale      optional device int8 [T][ldq], fp32 [T] (out): both or
+ *                 neither; out or q must be given.
+ * A row with a value or a sum of squares that is not finite has out NaN, codes
+ * 0 and scale NaN.  Other overlaps of the arrays are undefined.  16-byte bases
+ * and row strides (q: 8-byte) take the faster vector path.  No workspace. */
+MOE_Q4_API int moe_q4_add_norm(const void* x, int x_type, long long ldx, const void* residual, int residual_type,
+                               long long ldr, void* residual_out, long long ldro, const void* weight,
+                               int weight_type, float eps, int T, int H, void* out, long long ldo, int8_t* q,
+                               long long ldq, float* scale, void* stream);
+
+/* moe_q4_linear_i8 -- the product of int8 rows and an int8 weight matrix:
+ *   out[t][n] = x_scale[t] * w_scale[n] * sum_k x[t][k] * w[n][k] (+ bias[n]),
+ * sums exact in int32 (any int8 codes, -128 among them), the rest in fp32, the
+ * result rounded to out's type.  Deterministic; a row's result does not depend
+ * on the other rows of the call.
+ *   x        device int8 [T][ldx];   x_scale  device fp32 [T];
+ *   w        device int8 [N][ldw];   w_scale  device fp32 [N];
+ *   bias     optional device fp32 [N];
+ *   T >= 0; N >= 1; 1 <= K <= 131071 (MOE_Q4_ENOTSUP above: int32 sums);
+ *   out      device, bf16 or fp32 (out_type) [T][ldo] (out), aligned to its
+ *            elements.
+ * No workspace. */
+MOE_Q4_API int moe_q4_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w, long long ldw,
+                                const float* w_scale, const float* bias, int T, int N, int K, void* out,
+                                int out_type, long long ldo, void* stream);
+
+/* A SwiGLU MLP with int8 weights: the shared expert, or a dense layer's
+ * feed-forward, in int8.  Device pointers are borrowed for each call. */
+typedef struct moe_q4_mlp {
+  int H;                       /* hidden size */
+  int I;                       /* intermediate size */
+  const int8_t* gate_up;       /* device [2I][ld_gate_up]: rows 0..I-1 the gate, I..2I-1 the up projection */
+  long long ld_gate_up;        /* >= H */
+  const float* gate_up_scale;  /* device [2I] */
+  const int8_t* down;          /* device [H][ld_down] */
+  long long ld_down;           /* >= I */
+  const float* down_scale;     /* device [H] */
+} moe_q4_mlp;
+
+/* moe_q4_mlp_i8 -- out[t] = W_down (silu(W_gate x_t) * (W_up x_t)) for int8
+ * rows x: g and u as moe_q4_linear_i8 in fp32, h = bf16(silu(g) * u), the rows
+ * of h to codes and scales as moe_q4_quant_rows, and the down product of
+ * those as moe_q4_linear_i8.
+ *   x, x_scale  device int8 [T][ldx] and fp32 [T], rows of H codes;
+ *   out         device, bf16 or fp32 (out_type) [T][ldo] (out);
+ *   ws          device workspace, 256-byte aligned, of at least
+ *               moe_q4_mlp_i8_workspace(mlp, T) bytes (0 if the arguments are
+ *               invalid or T is 0), owned by the call until its work is done.
+ * H, I <= 131071 (MOE_Q4_ENOTSUP above). */
+MOE_Q4_API size_t moe_q4_mlp_i8_workspace(const moe_q4_mlp* mlp, int T);
+MOE_Q4_API int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long ldx, const float* x_scale, int T,
+                             void* out, int out_type, long long ldo, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_q4_forward_ex / moe_q4_forward_gated with the shared expert as an int8
+ * MLP (shared->H == layer->H): its output is added after the k routed slots in
+ * fp32.  The routed experts and the router gate read x as before; the MLP
+ * reads
+ *   xq, x_scale  optional device int8 [T][ldxq] and fp32 [T], the codes and
+ *                scales of the rows of x (as moe_q4_add_norm gives them beside
+ *                x): both or neither.  NULL: x is brought to int8 here, as
+ *                moe_q4_quant_rows does.
+ * The other arguments, errors and the status word are those of the calls with
+ * a bf16 shared expert. */
+MOE_Q4_API size_t moe_q4_forward_ex_i8_workspace(const moe_q4_layer* layer, const moe_q4_mlp* shared, int T,
+                                                 int top_k);
+MOE_Q4_API int moe_q4_forward_ex_i8(const moe_q4_layer* layer, const moe_q4_mlp* shared, const void* x,
+                                    const int8_t* xq, long long ldxq, const float* x_scale, const float* logits,
+                                    int T, int top_k, void* out, float* out_f32, int32_t* topk_ids, float* topk_w,
+                                    int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+MOE_Q4_API size_t moe_q4_forward_gated_i8_workspace(const moe_q4_layer* layer, const moe_q4_mlp* shared, int T,
+                                                    int top_k);
+MOE_Q4_API int moe_q4_forward_gated_i8(const moe_q4_layer* layer, const moe_q4_mlp* shared, const void* router_w,
+                                       const void* x, const int8_t* xq, long long ldxq, const float* x_scale, int T,
+                                       int top_k, void* out, float* out_f32, float* logits, int32_t* topk_ids,
+                                       float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * moe_q4_selftest_wait -- test support: checks that a bounded device wait
  * gives up and reports instead of hanging.  One CTA: a producer warp that
  * issues nothing and a consumer warp waiting on the stage barrier it would
