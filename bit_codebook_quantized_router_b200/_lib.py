@@ -100,9 +100,9 @@ def lib():
         L.moe_q4_quant_rows.argtypes = [vp, ci, ll, ci, ci, vp, ll, vp, vp]
         L.moe_q4_add_norm.argtypes = [vp, ci, ll, vp, ci, ll, vp, ll, vp, ci, ctypes.c_float, ci, ci, vp, ll, vp, ll,
                                       vp, vp]
-        L.moe_q4_linear_i8.argtypes = [vp, ll, vp, vp, ll, vp, vp, ci, ci, ci, vp, ci, ll, vp]
+        L.moe_q4_linear_i8.argtypes = [vp, ll, vp, vp, ll, vp, vp, ci, ci, ci, vp, ci, ll, vp, vp]
         L.moe_q4_mlp_i8_workspace.argtypes = [mlp, ci]
-        L.moe_q4_mlp_i8.argtypes = [mlp, vp, ll, vp, ci, vp, ci, ll, vp, sz, vp]
+        L.moe_q4_mlp_i8.argtypes = [mlp, vp, ll, vp, ci, vp, ci, ll, vp, vp, sz, vp]
         layer = ctypes.POINTER(_LayerStruct)
         L.moe_q4_forward_ex_i8_workspace.argtypes = [layer, mlp, ci, ci]
         L.moe_q4_forward_ex_i8.argtypes = [layer, mlp, vp, vp, ll, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -611,11 +611,12 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
 
 def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
               bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
-              dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+              dtype: torch.dtype = torch.bfloat16, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Int8 rows x [T, K] with scales x_scale [T] times int8 weights w [N, K]
     with scales w_scale [N], sums exact in int32: out [T, N] in bf16 or fp32
     (dtype, or out's), plus an fp32 bias [N].  The rows of x and w start on
-    16-byte boundaries (quant_rows makes them so)."""
+    16-byte boundaries (quant_rows makes them so).  status: an int32 CUDA
+    tensor [1] that receives the code of a device wait that gave up."""
     ldx = _row_stride(x, "x", (torch.int8,), pad=16)
     T, K = x.shape
     ldw = _row_stride(w, "w", (torch.int8,), cols=K, pad=16)
@@ -624,11 +625,13 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     if own:
         out = torch.empty((T, N), dtype=dtype, device=x.device)
     ldo = _row_stride(out, "out", _ROW_TYPE, N, T)
-    with _On(stream, x, x_scale, w, w_scale, bias, out) as h:
+    with _On(stream, x, x_scale, w, w_scale, bias, out, status) as h:
         _check(lib().moe_q4_linear_i8(x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), w.data_ptr(), ldw,
                                       _vector(w_scale, "w_scale", N),
                                       None if bias is None else _vector(bias, "bias", N), T, N, K, out.data_ptr(),
-                                      _ROW_TYPE[out.dtype], ldo, h), "moe_q4_linear_i8")
+                                      _ROW_TYPE[out.dtype], ldo,
+                                      None if status is None else _vector(status, "status", 1, (torch.int32,)), h),
+               "moe_q4_linear_i8")
     _hold(stream, out if own else None)
     return out
 
@@ -659,9 +662,10 @@ def mlp_i8_workspace(mlp: MlpI8, T: int) -> int:
 
 
 def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor | None = None,
-           dtype: torch.dtype = torch.bfloat16, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+           dtype: torch.dtype = torch.bfloat16, ws: torch.Tensor | None = None, status: torch.Tensor | None = None,
+           stream=None) -> torch.Tensor:
     """The int8 SwiGLU MLP: int8 rows x [T, H] with scales x_scale [T] -> out
-    [T, H] in bf16 or fp32 (dtype, or out's)."""
+    [T, H] in bf16 or fp32 (dtype, or out's); status as for linear_i8."""
     ldx = _row_stride(x, "x", (torch.int8,), mlp.H, pad=16)
     T = x.shape[0]
     own, own_ws = out is None, ws is None
@@ -670,9 +674,11 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
     if own_ws:
         ws = alloc_workspace(mlp_i8_workspace(mlp, T), x.device)
     ldo = _row_stride(out, "out", _ROW_TYPE, mlp.H, T)
-    with _On(stream, x, x_scale, out, ws, mlp.tensors[0]) as h:
+    with _On(stream, x, x_scale, out, ws, status, mlp.tensors[0]) as h:
         _check(lib().moe_q4_mlp_i8(mlp.ref, x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), T, out.data_ptr(),
-                                   _ROW_TYPE[out.dtype], ldo, ws.data_ptr(), ws.numel(), h), "moe_q4_mlp_i8")
+                                   _ROW_TYPE[out.dtype], ldo,
+                                   None if status is None else _vector(status, "status", 1, (torch.int32,)),
+                                   ws.data_ptr(), ws.numel(), h), "moe_q4_mlp_i8")
     _hold(stream, out if own else None, ws if own_ws else None)
     return out
 

@@ -318,8 +318,8 @@ int run_forward(const moe_q4_layer* L, const TableParams& tp, const void* x, con
       ldxq = L->H;
     }
     if (rc == MOE_Q4_OK)
-      rc = moe_q4_mlp_i8(S8->mlp, xq, ldxq, xs, T, ws + o.y_s, MOE_Q4_F32, L->H, ws + o.mlp_ws,
-                         moe_q4_mlp_i8_workspace(S8->mlp, T), s);
+      rc = moe_q4_mlp_i8(S8->mlp, xq, ldxq, xs, T, ws + o.y_s, MOE_Q4_F32, L->H, a.hdr + kStatus,
+                         ws + o.mlp_ws, moe_q4_mlp_i8_workspace(S8->mlp, T), s);
   }
   if (rc == MOE_Q4_OK) rc = mark(6);
   if (rc == MOE_Q4_OK) rc = q4_launch_combine(a, s);

@@ -7,35 +7,15 @@
 // 131,071 cannot overflow, and they do not depend on the order or on how K is
 // split.  The one rounding of a sum is its conversion to fp32; the product of
 // the scales and the result's are one each, and the result's type is the last.
-#include "q4_api_internal.h"
-#include "q4_common.cuh"
+#include "linear8.cuh"
 
 namespace q4 {
 
 namespace {
 
-constexpr int kMaxK = 131071;  // 2^14 * K < 2^31
-
-struct LinArgs {
-  const int8_t* x;       // [T][ldx]
-  const float* xs;       // [T]
-  const int8_t* w;       // [N][ldw], gated: [2 N][ldw], the gate's rows first
-  const float* ws;       // [N], gated: [2 N]
-  const float* bias;     // [N] or null
-  void* out;             // [T][ldo], bf16 or fp32
-  long long ldx, ldw, ldo;
-  int T, N, K;
-  int out_f32;
-};
-
-__device__ __forceinline__ float scaled(int acc, float xs, float ws) { return (float)acc * (xs * ws); }
-
-__device__ __forceinline__ void store_out(const LinArgs& a, int t, int n, float v) {
-  if (a.out_f32)
-    reinterpret_cast<float*>(a.out)[t * a.ldo + n] = v;
-  else
-    reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.ldo + n] = __float2bfloat16_rn(v);
-}
+constexpr int kMaxK = 131071;          // 2^14 * K < 2^31
+constexpr int kMaxRows = 1 << 30;      // tokens or channels of a product (tile arithmetic in 32 bits)
+constexpr int kFewTokens = 16;         // the most that few_kernel takes
 
 // D += A(16x32, int8, row) * B(32x8, int8, col), int32.
 __device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -65,7 +45,6 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int n0 = blockIdx.x * (GATED ? 8 : 16);
-  const int t0 = blockIdx.y * 8 * NT;
   const int ra = min(n0 + g, a.N - 1);
   const int rb = GATED ? a.N + ra : min(n0 + g + 8, a.N - 1);
   const int8_t* wa = a.w + ra * a.ldw;
@@ -75,7 +54,7 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArg
     const uint4 va = load_row16(wa, k, a.K), vb = load_row16(wb, k, a.K);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int t = t0 + 8 * n + g;
+      const int t = 8 * n + g;
       const uint4 b = t < a.T ? load_row16(a.x + t * a.ldx, k, a.K) : make_uint4(0, 0, 0, 0);
       mma_s8(acc[n], va.x, vb.x, va.y, vb.y, b.x, b.y);
       mma_s8(acc[n], va.z, vb.z, va.w, vb.w, b.z, b.w);
@@ -89,7 +68,7 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArg
   __syncthreads();
   constexpr int kRows = GATED ? 8 : 16;
   for (int i = threadIdx.x; i < 8 * NT * kRows; i += blockDim.x) {
-    const int col = i / kRows, r = i % kRows, t = t0 + col, n = n0 + r;
+    const int col = i / kRows, r = i % kRows, t = col, n = n0 + r;
     if (t >= a.T || n >= a.N) continue;
     int v = 0, u = 0;
     for (int w = 0; w < warps; ++w) {
@@ -105,15 +84,28 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArg
   }
 }
 
-template <bool GATED>
-int launch_linear(const LinArgs& a, cudaStream_t s) {
-  const int rows = GATED ? 8 : 16;
-  const dim3 grid((a.N + rows - 1) / rows, (a.T + 31) / 32);
-  if (a.T <= 8)
-    few_kernel<1, GATED><<<dim3(grid.x, 1), 256, 8 * 8 * 16 * 4, s>>>(a);
-  else
-    few_kernel<4, GATED><<<grid, 256, 8 * 32 * 16 * 4, s>>>(a);
+int launch_few(const LinArgs& a, bool gated, cudaStream_t s) {
+  const int rows = gated ? 8 : 16, nt = a.T <= 8 ? 1 : 2;
+  const unsigned grid = (a.N + rows - 1) / rows;
+  const int smem = 8 * 8 * nt * 16 * 4;
+  if (nt == 1) {
+    if (gated)
+      few_kernel<1, true><<<grid, 256, smem, s>>>(a);
+    else
+      few_kernel<1, false><<<grid, 256, smem, s>>>(a);
+  } else {
+    if (gated)
+      few_kernel<2, true><<<grid, 256, smem, s>>>(a);
+    else
+      few_kernel<2, false><<<grid, 256, smem, s>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+}
+
+int launch_linear(const LinArgs& a, bool gated, cudaStream_t s) {
+  if (a.T <= kFewTokens) return launch_few(a, gated, s);
+  if (a.T <= kLinearMidTokens) return q4_launch_linear_mid(a, gated, s);
+  return q4_launch_linear_wide(a, gated, s);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -159,16 +151,16 @@ using namespace q4;
 
 extern "C" int moe_q4_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w, long long ldw,
                                 const float* w_scale, const float* bias, int T, int N, int K, void* out,
-                                int out_type, long long ldo, void* stream) {
+                                int out_type, long long ldo, int32_t* status, void* stream) {
   if (T < 0 || N < 1 || K < 1 || ldx < K || ldw < K || ldo < N) return MOE_Q4_EINVAL;
   if (out_type != MOE_Q4_BF16 && out_type != MOE_Q4_F32) return MOE_Q4_EINVAL;
-  if (K > kMaxK) return MOE_Q4_ENOTSUP;
+  if (K > kMaxK || T > kMaxRows || N > kMaxRows) return MOE_Q4_ENOTSUP;
   if (T == 0) return MOE_Q4_OK;
   if (!rows16(x, ldx) || !rows16(w, ldw) || !floats(x_scale) || !floats(w_scale) || ((uintptr_t)bias & 3) || !out ||
-      ((uintptr_t)out & (out_type == MOE_Q4_F32 ? 3 : 1)))
+      ((uintptr_t)out & (out_type == MOE_Q4_F32 ? 3 : 1)) || ((uintptr_t)status & 3))
     return MOE_Q4_EINVAL;
-  const LinArgs a = {x, x_scale, w, w_scale, bias, out, ldx, ldw, ldo, T, N, K, out_type == MOE_Q4_F32};
-  return launch_linear<false>(a, (cudaStream_t)stream);
+  const LinArgs a = {x, x_scale, w, w_scale, bias, out, status, ldx, ldw, ldo, T, N, K, out_type == MOE_Q4_F32};
+  return launch_linear(a, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t moe_q4_mlp_i8_workspace(const moe_q4_mlp* mlp, int T) {
@@ -177,26 +169,29 @@ extern "C" size_t moe_q4_mlp_i8_workspace(const moe_q4_mlp* mlp, int T) {
 }
 
 extern "C" int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long ldx, const float* x_scale, int T,
-                             void* out, int out_type, long long ldo, void* ws, size_t ws_bytes, void* stream) {
+                             void* out, int out_type, long long ldo, int32_t* status, void* ws, size_t ws_bytes,
+                             void* stream) {
   int rc = mlp_check(mlp);
   if (rc != MOE_Q4_OK) return rc;
   if (T < 0 || ldx < mlp->H || ldo < mlp->H || (out_type != MOE_Q4_BF16 && out_type != MOE_Q4_F32))
     return MOE_Q4_EINVAL;
+  if (T > kMaxRows) return MOE_Q4_ENOTSUP;
   if (T == 0) return MOE_Q4_OK;
-  if (!rows16(x, ldx) || !floats(x_scale) || !out || ((uintptr_t)out & (out_type == MOE_Q4_F32 ? 3 : 1)))
+  if (!rows16(x, ldx) || !floats(x_scale) || !out || ((uintptr_t)out & (out_type == MOE_Q4_F32 ? 3 : 1)) ||
+      ((uintptr_t)status & 3))
     return MOE_Q4_EINVAL;
   const MlpLayout o = mlp_layout(mlp->I, T);
   if (!ws || ((uintptr_t)ws & 255) || ws_bytes < o.end) return MOE_Q4_EWORKSPACE;
   char* p = (char*)ws;
   const cudaStream_t s = (cudaStream_t)stream;
-  const LinArgs gu = {x, x_scale, mlp->gate_up, mlp->gate_up_scale, nullptr, p + o.h, ldx, mlp->ld_gate_up, o.ldh,
-                      T, mlp->I, mlp->H, 0};
-  rc = launch_linear<true>(gu, s);
+  const LinArgs gu = {x, x_scale, mlp->gate_up, mlp->gate_up_scale, nullptr, p + o.h, status, ldx, mlp->ld_gate_up,
+                      o.ldh, T, mlp->I, mlp->H, 0};
+  rc = launch_linear(gu, true, s);
   if (rc == MOE_Q4_OK)
     rc = moe_q4_quant_rows(p + o.h, MOE_Q4_BF16, o.ldh, T, mlp->I, (int8_t*)(p + o.q), o.ldq, (float*)(p + o.scale),
                            stream);
   if (rc != MOE_Q4_OK) return rc;
   const LinArgs dn = {(const int8_t*)(p + o.q), (const float*)(p + o.scale), mlp->down, mlp->down_scale, nullptr, out,
-                      o.ldq, mlp->ld_down, ldo, T, mlp->H, mlp->I, out_type == MOE_Q4_F32};
-  return launch_linear<false>(dn, s);
+                      status, o.ldq, mlp->ld_down, ldo, T, mlp->H, mlp->I, out_type == MOE_Q4_F32};
+  return launch_linear(dn, false, s);
 }

@@ -1,0 +1,38 @@
+// What the kernels of the int8 products share.
+#pragma once
+
+#include "q4_api_internal.h"
+#include "q4_common.cuh"
+
+namespace q4 {
+
+struct LinArgs {
+  const int8_t* x;       // [T][ldx]
+  const float* xs;       // [T]
+  const int8_t* w;       // [N][ldw], gated: [2 N][ldw], the gate's rows first
+  const float* ws;       // [N], gated: [2 N]
+  const float* bias;     // [N] or null
+  void* out;             // [T][ldo], bf16 or fp32
+  int32_t* status;       // or null
+  long long ldx, ldw, ldo;
+  int T, N, K;
+  int out_f32;
+};
+
+// The one place that turns a sum into a value: the same bits in every kernel.
+__device__ __forceinline__ float scaled(int acc, float xs, float ws) { return (float)acc * (xs * ws); }
+
+__device__ __forceinline__ void store_out(const LinArgs& a, long long t, int n, float v) {
+  if (a.out_f32)
+    reinterpret_cast<float*>(a.out)[t * a.ldo + n] = v;
+  else
+    reinterpret_cast<__nv_bfloat16*>(a.out)[t * a.ldo + n] = __float2bfloat16_rn(v);
+}
+
+}  // namespace q4
+
+// linear8_tc.cu: products on the tensor cores, for a moderate number of
+// tokens (K split over a cluster) and for many (CTA pairs).
+int q4_launch_linear_mid(const q4::LinArgs& a, bool gated, cudaStream_t s);
+int q4_launch_linear_wide(const q4::LinArgs& a, bool gated, cudaStream_t s);
+constexpr int kLinearMidTokens = 256;  // the most that q4_launch_linear_mid takes

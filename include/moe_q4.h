@@ -489,11 +489,14 @@ MOE_Q4_API int moe_q4_add_norm(const void* x, int x_type, long long ldx, const v
  *   bias     optional device fp32 [N];
  *   T >= 0; N >= 1; 1 <= K <= 131071 (MOE_Q4_ENOTSUP above: int32 sums);
  *   out      device, bf16 or fp32 (out_type) [T][ldo] (out), aligned to its
- *            elements.
- * No workspace. */
+ *            elements;
+ *   status   optional device int32 (in/out), NULL to skip: left unchanged,
+ *            or MOE_Q4_ETIMEOUT where it was MOE_Q4_OK if a bounded device
+ *            wait gave up (out is then unspecified; moe_q4_read_status).
+ * T, N <= 2^30 (MOE_Q4_ENOTSUP above).  No workspace. */
 MOE_Q4_API int moe_q4_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w, long long ldw,
                                 const float* w_scale, const float* bias, int T, int N, int K, void* out,
-                                int out_type, long long ldo, void* stream);
+                                int out_type, long long ldo, int32_t* status, void* stream);
 
 /* A SwiGLU MLP with int8 weights: the shared expert, or a dense layer's
  * feed-forward, in int8.  Device pointers are borrowed for each call. */
@@ -514,13 +517,15 @@ typedef struct moe_q4_mlp {
  * those as moe_q4_linear_i8.
  *   x, x_scale  device int8 [T][ldx] and fp32 [T], rows of H codes;
  *   out         device, bf16 or fp32 (out_type) [T][ldo] (out);
+ *   status      as for moe_q4_linear_i8;
  *   ws          device workspace, 256-byte aligned, of at least
  *               moe_q4_mlp_i8_workspace(mlp, T) bytes (0 if the arguments are
  *               invalid or T is 0), owned by the call until its work is done.
- * H, I <= 131071 (MOE_Q4_ENOTSUP above). */
+ * H, I <= 131071, T <= 2^30 (MOE_Q4_ENOTSUP above). */
 MOE_Q4_API size_t moe_q4_mlp_i8_workspace(const moe_q4_mlp* mlp, int T);
 MOE_Q4_API int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long ldx, const float* x_scale, int T,
-                             void* out, int out_type, long long ldo, void* ws, size_t ws_bytes, void* stream);
+                             void* out, int out_type, long long ldo, int32_t* status, void* ws, size_t ws_bytes,
+                             void* stream);
 
 /* moe_q4_forward_ex / moe_q4_forward_gated with the shared expert as an int8
  * MLP (shared->H == layer->H): its output is added after the k routed slots in

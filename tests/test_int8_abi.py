@@ -44,15 +44,16 @@ def test_add_norm_refusals(L):
 
 
 def test_linear_refusals(L):
-    ok = dict(x=P, ldx=64, xs=P, w=Q, ldw=64, ws=P, bias=None, T=4, N=8, K=64, out=P, ot=BF16, ldo=8, stream=None)
+    ok = dict(x=P, ldx=64, xs=P, w=Q, ldw=64, ws=P, bias=None, T=4, N=8, K=64, out=P, ot=BF16, ldo=8, status=None, stream=None)
     f = lambda **k: L.moe_q4_linear_i8(*{**ok, **k}.values())  # noqa: E731
     for bad in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(out=None), dict(T=-1), dict(N=0),
                 dict(K=0), dict(ldx=48), dict(ldx=72), dict(ldw=48), dict(ldw=72), dict(ldo=7), dict(ot=2),
                 dict(x=P + 8), dict(w=Q + 8), dict(xs=P + 2), dict(ws=P + 2), dict(bias=P + 2), dict(out=P + 1),
-                dict(out=P + 2, ot=F32)):
+                dict(out=P + 2, ot=F32), dict(status=P + 2)):
         assert f(**bad) == _lib.EINVAL, bad
     # int32 sums of any codes: K to 131071
     assert f(K=131072, ldx=131072, ldw=131072) == _lib.ENOTSUP
+    assert f(T=(1 << 30) + 1) == f(N=(1 << 30) + 1, ldo=1 << 31) == _lib.ENOTSUP
     assert f(T=0, x=None, out=None) == _lib.OK
 
 
@@ -64,7 +65,7 @@ def test_mlp_refusals(L):
     n = L.moe_q4_mlp_i8_workspace(ctypes.byref(_mlp()), 4)
     assert n > 0 and L.moe_q4_mlp_i8_workspace(ctypes.byref(_mlp()), 0) == 0
     assert L.moe_q4_mlp_i8_workspace(None, 4) == 0
-    ok = dict(x=P, ldx=64, xs=P, T=4, out=P, ot=BF16, ldo=64, ws=P, n=n, stream=None)
+    ok = dict(x=P, ldx=64, xs=P, T=4, out=P, ot=BF16, ldo=64, status=None, ws=P, n=n, stream=None)
     f = lambda m=_mlp(), **k: L.moe_q4_mlp_i8(ctypes.byref(m), *{**ok, **k}.values())  # noqa: E731
     for m in (_mlp(H=0), _mlp(I=0), _mlp(gu=None), _mlp(dn=None), _mlp(gus=None), _mlp(ds=None), _mlp(ldg=48),
               _mlp(ldg=72), _mlp(ldd=16), _mlp(ldd=40), _mlp(gu=P + 8), _mlp(ds=P + 1)):
@@ -72,7 +73,7 @@ def test_mlp_refusals(L):
         assert f(m) == _lib.EINVAL
     assert f(_mlp(I=131072, ldd=131072)) == _lib.ENOTSUP
     for bad in (dict(x=None), dict(xs=None), dict(out=None), dict(T=-1), dict(ldx=48), dict(ldx=72), dict(ldo=63),
-                dict(ot=5), dict(x=P + 8), dict(out=P + 1), dict(xs=P + 1)):
+                dict(ot=5), dict(x=P + 8), dict(out=P + 1), dict(xs=P + 1), dict(status=P + 1)):
         assert f(**bad) == _lib.EINVAL, bad
     for bad in (dict(ws=None), dict(ws=P + 128), dict(n=n - 1)):
         assert f(**bad) == _lib.EWORKSPACE, bad
