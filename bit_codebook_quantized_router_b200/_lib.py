@@ -486,78 +486,78 @@ def combine(y: torch.Tensor, w: torch.Tensor, inv=None, out=None, out_f32=None, 
 # ---- 8-bit integer rows, products and the int8 MLP -------------------------
 
 _ROW_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+_INT8, _BF16, _FP32, _INT32 = (torch.int8,), (torch.bfloat16,), (torch.float32,), (torch.int32,)
+# the current stream's handle without building a Stream object (a few us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _row_stride(t, what, dtypes=_ROW_TYPE, cols=None, rows=None, pad=1):
-    """Check a CUDA matrix of consecutive elements in each row; its row stride
+def _device(t):
+    dev = t.get_device()
+    if dev < 0 or t.dim() != 2:
+        raise ValueError("the operands must be CUDA matrices")
+    return dev
+
+
+def _rows(t, what, dev, n, k, dtypes):
+    """Check a [n, k] matrix of consecutive elements in each row; its row stride
     in elements (that of a single row is of no consequence)."""
-    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA matrix of {' or '.join(str(d) for d in dtypes)}")
-    n, k = t.shape
-    if (cols is not None and k != cols) or (rows is not None and n != rows):
-        raise ValueError(f"{what} must be [{n if rows is None else rows}, {k if cols is None else cols}], "
-                         f"not [{n}, {k}]")
-    ld, inner = t.stride()
-    if inner != 1 and k > 1:
-        raise ValueError(f"{what}: the elements of a row must be consecutive")
-    if n > 1:
-        return ld
-    return -(-k // pad) * pad
+    shape, (ld, inner) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
+    if shape != (n, k) or t.dtype not in dtypes or t.get_device() != dev or (inner != 1 and k > 1):
+        raise ValueError(f"{what} must be a matrix [{n}, {k}] of {' or '.join(str(d) for d in dtypes)} with "
+                         f"consecutive elements in a row, on cuda:{dev}; not {t.dtype} {list(shape)} with strides "
+                         f"{t.stride()} on {t.device}")
+    return ld if n > 1 else -(-k // 16) * 16
 
 
-def _vector(t, what, n, dtypes=(torch.float32,)):
-    if t.dim() != 1 or t.dtype not in dtypes or not t.is_cuda or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA vector of {n} {' or '.join(str(d) for d in dtypes)}")
+def _vector(t, what, dev, n, dtypes=_FP32):
+    if t.shape != (n,) or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n} {' or '.join(str(d) for d in dtypes)} on "
+                         f"cuda:{dev}; not {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-class _On:
-    """The device of a call's tensors as the current one, and the stream's handle."""
-
-    def __init__(self, stream, first, *others):
-        dev = first.device
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError("the tensors of a call must be on one device")
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError("the stream must be of the tensors' device")
-        self.handle = stream.cuda_stream
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(what, dev, stream, made, fn, *args):
+    """fn(*args, stream handle) with the tensors' device as the current one.
+    `made`: what the binding allocated for the call (see _hold)."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream must be of the tensors' device, cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != OK:
+        raise MoeQ4Error(rc, what)
+    if stream is not None:
+        _hold(stream, *made)
 
 
-def _codes(T, K, device):
+def _codes(T, K, dev):
     """An int8 [T, K] whose rows start on 16 bytes, as the products read them."""
-    return torch.empty((T, -(-K // 16) * 16), dtype=torch.int8, device=device)[:, :K]
+    return torch.empty((T, -(-K // 16) * 16), dtype=torch.int8, device=dev)[:, :K]
 
 
 def quant_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """bf16 or fp32 rows x [T, K] -> (codes int8 [T, K], scales fp32 [T]): for
     each row scale = max|x| / 127 and the codes nearest to 127 x / max|x|, ties
     to even.  A new q has rows on 16-byte boundaries (linear_i8's operands)."""
-    ldx = _row_stride(x, "x")
+    dev = _device(x)
     T, K = x.shape
-    new = q is None, scale is None
-    if new[0]:
+    ldx = _rows(x, "x", dev, T, K, _ROW_TYPE)
+    made = []
+    if q is None:
         q = _codes(T, K, x.device)
-    if new[1]:
+        made.append(q)
+    if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=x.device)
-    ldq = _row_stride(q, "q", (torch.int8,), K, T)
-    sp = _vector(scale, "scale", T)
-    with _On(stream, x, q, scale) as h:
-        _check(lib().moe_q4_quant_rows(x.data_ptr(), _ROW_TYPE[x.dtype], ldx, T, K, q.data_ptr(), ldq, sp, h),
-               "moe_q4_quant_rows")
-    _hold(stream, q if new[0] else None, scale if new[1] else None)
+        made.append(scale)
+    _call("moe_q4_quant_rows", dev, stream, made, lib().moe_q4_quant_rows, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, T, K,
+          q.data_ptr(), _rows(q, "q", dev, T, K, _INT8), _vector(scale, "scale", dev, T))
     return q, scale
 
 
@@ -572,40 +572,38 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
     residual, out bf16 [T, H] or None with bf16=False, codes int8 [T, H] and
     scales fp32 [T] or None with quant=False).  residual_out may be residual
     itself (in place), out may be a bf16 x."""
-    ldx = _row_stride(x, "x")
+    dev = _device(x)
     T, H = x.shape
-    dev = x.device
+    ldx = _rows(x, "x", dev, T, H, _ROW_TYPE)
     made = []
-
-    def own(t):
-        made.append(t)
-        return t
-
     ldr = ldro = ldo = ldq = rt = wt = 0
     rp = rop = wp = op = qp = sp = None
     if residual is not None:
-        ldr, rt, rp = _row_stride(residual, "residual", cols=H, rows=T), _ROW_TYPE[residual.dtype], residual.data_ptr()
+        dtype = residual.dtype
+        ldr, rp = _rows(residual, "residual", dev, T, H, _ROW_TYPE), residual.data_ptr()
         if residual_out is None:
-            residual_out = own(torch.empty((T, H), dtype=residual.dtype, device=dev))
-        ldro, rop = _row_stride(residual_out, "residual_out", (residual.dtype,), H, T), residual_out.data_ptr()
+            residual_out = torch.empty((T, H), dtype=dtype, device=x.device)
+            made.append(residual_out)
+        ldro, rop, rt = _rows(residual_out, "residual_out", dev, T, H, (dtype,)), residual_out.data_ptr(), _ROW_TYPE[dtype]
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if weight is not None:
-        wp, wt = _vector(weight, "weight", H, _ROW_TYPE), _ROW_TYPE[weight.dtype]
+        wp, wt = _vector(weight, "weight", dev, H, _ROW_TYPE), _ROW_TYPE[weight.dtype]
     if bf16 or out is not None:
         if out is None:
-            out = own(torch.empty((T, H), dtype=torch.bfloat16, device=dev))
-        ldo, op = _row_stride(out, "out", (torch.bfloat16,), H, T), out.data_ptr()
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            made.append(out)
+        ldo, op = _rows(out, "out", dev, T, H, _BF16), out.data_ptr()
     if quant or q is not None or scale is not None:
         if q is None:
-            q = own(_codes(T, H, dev))
+            q = _codes(T, H, x.device)
+            made.append(q)
         if scale is None:
-            scale = own(torch.empty(T, dtype=torch.float32, device=dev))
-        ldq, qp, sp = _row_stride(q, "q", (torch.int8,), H, T), q.data_ptr(), _vector(scale, "scale", T)
-    with _On(stream, x, residual, residual_out, weight, out, q, scale) as h:
-        _check(lib().moe_q4_add_norm(x.data_ptr(), _ROW_TYPE[x.dtype], ldx, rp, rt, ldr, rop, ldro, wp, wt,
-                                     eps, T, H, op, ldo, qp, ldq, sp, h), "moe_q4_add_norm")
-    _hold(stream, *made)
+            scale = torch.empty(T, dtype=torch.float32, device=x.device)
+            made.append(scale)
+        ldq, qp, sp = _rows(q, "q", dev, T, H, _INT8), q.data_ptr(), _vector(scale, "scale", dev, T)
+    _call("moe_q4_add_norm", dev, stream, made, lib().moe_q4_add_norm, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, rp, rt,
+          ldr, rop, ldro, wp, wt, eps, T, H, op, ldo, qp, ldq, sp)
     return residual_out, out, q, scale
 
 
@@ -617,22 +615,19 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     (dtype, or out's), plus an fp32 bias [N].  The rows of x and w start on
     16-byte boundaries (quant_rows makes them so).  status: an int32 CUDA
     tensor [1] that receives the code of a device wait that gave up."""
-    ldx = _row_stride(x, "x", (torch.int8,), pad=16)
+    dev = _device(x)
     T, K = x.shape
-    ldw = _row_stride(w, "w", (torch.int8,), cols=K, pad=16)
     N = w.shape[0]
-    own = out is None
-    if own:
+    made = []
+    if out is None:
         out = torch.empty((T, N), dtype=dtype, device=x.device)
-    ldo = _row_stride(out, "out", _ROW_TYPE, N, T)
-    with _On(stream, x, x_scale, w, w_scale, bias, out, status) as h:
-        _check(lib().moe_q4_linear_i8(x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), w.data_ptr(), ldw,
-                                      _vector(w_scale, "w_scale", N),
-                                      None if bias is None else _vector(bias, "bias", N), T, N, K, out.data_ptr(),
-                                      _ROW_TYPE[out.dtype], ldo,
-                                      None if status is None else _vector(status, "status", 1, (torch.int32,)), h),
-               "moe_q4_linear_i8")
-    _hold(stream, out if own else None)
+        made.append(out)
+    _call("moe_q4_linear_i8", dev, stream, made, lib().moe_q4_linear_i8, x.data_ptr(),
+          _rows(x, "x", dev, T, K, _INT8), _vector(x_scale, "x_scale", dev, T), w.data_ptr(),
+          _rows(w, "w", dev, N, K, _INT8), _vector(w_scale, "w_scale", dev, N),
+          None if bias is None else _vector(bias, "bias", dev, N), T, N, K, out.data_ptr(),
+          _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, N, _ROW_TYPE),
+          None if status is None else _vector(status, "status", dev, 1, _INT32))
     return out
 
 
@@ -644,14 +639,14 @@ class MlpI8:
 
     def __init__(self, gate_up: torch.Tensor, gate_up_scale: torch.Tensor, down: torch.Tensor,
                  down_scale: torch.Tensor):
-        ldg = _row_stride(gate_up, "gate_up", (torch.int8,), pad=16)
-        if gate_up.shape[0] % 2:
+        dev = _device(gate_up)
+        n, self.H = gate_up.shape
+        if n % 2:
             raise ValueError("gate_up holds the gate's rows and as many rows of the up projection")
-        self.I, self.H = gate_up.shape[0] // 2, gate_up.shape[1]
-        ldd = _row_stride(down, "down", (torch.int8,), self.I, self.H, pad=16)
-        gp, dp = _vector(gate_up_scale, "gate_up_scale", 2 * self.I), _vector(down_scale, "down_scale", self.H)
-        if len({t.device for t in (gate_up, gate_up_scale, down, down_scale)}) != 1:
-            raise ValueError("the tensors of an MLP must be on one device")
+        self.I = n // 2
+        ldg = _rows(gate_up, "gate_up", dev, n, self.H, _INT8)
+        ldd = _rows(down, "down", dev, self.H, self.I, _INT8)
+        gp, dp = _vector(gate_up_scale, "gate_up_scale", dev, n), _vector(down_scale, "down_scale", dev, self.H)
         self.tensors = gate_up, gate_up_scale, down, down_scale
         self.struct = _MlpStruct(self.H, self.I, gate_up.data_ptr(), ldg, gp, down.data_ptr(), ldd, dp)
         self.ref = ctypes.byref(self.struct)
@@ -666,20 +661,23 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
            stream=None) -> torch.Tensor:
     """The int8 SwiGLU MLP: int8 rows x [T, H] with scales x_scale [T] -> out
     [T, H] in bf16 or fp32 (dtype, or out's); status as for linear_i8."""
-    ldx = _row_stride(x, "x", (torch.int8,), mlp.H, pad=16)
-    T = x.shape[0]
-    own, own_ws = out is None, ws is None
-    if own:
-        out = torch.empty((T, mlp.H), dtype=dtype, device=x.device)
-    if own_ws:
+    dev = _device(x)
+    T, H = x.shape[0], mlp.H
+    made = []
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=x.device)
+        made.append(out)
+    if ws is None:
         ws = alloc_workspace(mlp_i8_workspace(mlp, T), x.device)
-    ldo = _row_stride(out, "out", _ROW_TYPE, mlp.H, T)
-    with _On(stream, x, x_scale, out, ws, status, mlp.tensors[0]) as h:
-        _check(lib().moe_q4_mlp_i8(mlp.ref, x.data_ptr(), ldx, _vector(x_scale, "x_scale", T), T, out.data_ptr(),
-                                   _ROW_TYPE[out.dtype], ldo,
-                                   None if status is None else _vector(status, "status", 1, (torch.int32,)),
-                                   ws.data_ptr(), ws.numel(), h), "moe_q4_mlp_i8")
-    _hold(stream, out if own else None, ws if own_ws else None)
+        made.append(ws)
+    elif ws.get_device() != dev or ws.dtype != torch.uint8:
+        raise ValueError(f"ws must be uint8 on cuda:{dev} (alloc_workspace)")
+    if mlp.tensors[0].get_device() != dev:
+        raise ValueError(f"the MLP's weights must be on cuda:{dev}")
+    _call("moe_q4_mlp_i8", dev, stream, made, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(),
+          _rows(x, "x", dev, T, H, _INT8), _vector(x_scale, "x_scale", dev, T), T, out.data_ptr(),
+          _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, H, _ROW_TYPE),
+          None if status is None else _vector(status, "status", dev, 1, _INT32), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -691,5 +689,6 @@ def _shared_rows(layer, shared, xq, x_scale, T):
         return 0
     if not isinstance(shared, MlpI8):
         raise ValueError("xq and x_scale are read by an int8 shared expert (MlpI8)")
-    _vector(x_scale, "x_scale", T)
-    return _row_stride(xq, "xq", (torch.int8,), layer.H, T, pad=16)
+    dev = _device(xq)
+    _vector(x_scale, "x_scale", dev, T)
+    return _rows(xq, "xq", dev, T, layer.H, _INT8)

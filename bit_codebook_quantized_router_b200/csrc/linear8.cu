@@ -34,12 +34,43 @@ __device__ __forceinline__ uint4 load_row16(const int8_t* row, int k, int K) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// U segments of 128 bytes of the rows at wa and wb, `stride` apart: every load
+// is under way before the first product.
+template <int NT, int U>
+__device__ __forceinline__ void few_step(const LinArgs& a, const int8_t* wa, const int8_t* wb, int sg, int stride, int g,
+                                         int t4, int acc[NT][4]) {
+  uint4 va[U][2], vb[U][2], b[U][2][NT];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = (sg + u * stride) * 128 + h * 64 + 16 * t4;
+      va[u][h] = ldg_stream(wa + k);
+      vb[u][h] = ldg_stream(wb + k);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int t = 8 * n + g;
+        b[u][h][n] = t < a.T ? ldg_nc(a.x + t * a.ldx + k) : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 p = va[u][h], q = vb[u][h], x = b[u][h][n];
+        mma_s8(acc[n], p.x, q.x, p.y, q.y, x.x, x.y);
+        mma_s8(acc[n], p.z, q.z, p.w, q.w, x.z, x.w);
+      }
+}
+
 // Few tokens: 16 weight rows a CTA (8 gate and 8 up rows when GATED), 8 NT
-// tokens, K split over the warps in segments of 64 bytes.  The weights go from
+// tokens, K split over the warps in segments of 128 bytes.  The weights go from
 // memory to the registers of the MMA with no stop: lane (g, t) holds 16 bytes
 // of rows g and g + 8 at byte 16 t of the segment, which are the A operands of
 // two MMAs once K is permuted the same way in the tokens' rows.
-template <int NT, bool GATED>
+template <int NT, int U, bool GATED>
 __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ int s_acc[];  // [warps][8 NT][16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -50,7 +81,11 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ LinArg
   const int8_t* wa = a.w + ra * a.ldw;
   const int8_t* wb = a.w + rb * a.ldw;
   int acc[NT][4] = {};
-  for (int k = warp * 64 + 16 * t4; k < a.K + 16 * t4; k += warps * 64) {
+  const int full = a.K / 128;  // whole segments of 128 bytes
+  int sg = warp;
+  for (; sg + (U - 1) * warps < full; sg += U * warps) few_step<NT, U>(a, wa, wb, sg, warps, g, t4, acc);
+  for (; sg < full; sg += warps) few_step<NT, 1>(a, wa, wb, sg, warps, g, t4, acc);
+  for (int k = full * 128 + warp * 64 + 16 * t4; k < a.K + 16 * t4; k += warps * 64) {
     const uint4 va = load_row16(wa, k, a.K), vb = load_row16(wb, k, a.K);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -90,14 +125,14 @@ int launch_few(const LinArgs& a, bool gated, cudaStream_t s) {
   const int smem = 8 * 8 * nt * 16 * 4;
   if (nt == 1) {
     if (gated)
-      few_kernel<1, true><<<grid, 256, smem, s>>>(a);
+      few_kernel<1, 3, true><<<grid, 256, smem, s>>>(a);
     else
-      few_kernel<1, false><<<grid, 256, smem, s>>>(a);
+      few_kernel<1, 3, false><<<grid, 256, smem, s>>>(a);
   } else {
     if (gated)
-      few_kernel<2, true><<<grid, 256, smem, s>>>(a);
+      few_kernel<2, 2, true><<<grid, 256, smem, s>>>(a);
     else
-      few_kernel<2, false><<<grid, 256, smem, s>>>(a);
+      few_kernel<2, 2, false><<<grid, 256, smem, s>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }

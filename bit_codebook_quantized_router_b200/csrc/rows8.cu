@@ -15,8 +15,11 @@
 // Exact quotient: 127 / m and its product with p are each rounded once, so
 // the product is within 127 * 2^-23 < 2e-5 of the quotient; one whose distance
 // from its nearest whole number is below 0.4999 has the quotient's rounding.
-// The others (2 in 10,000) are divided in 64 bits, where 127 p is exact and a
-// quotient that is no tie is at least 2^-25 from one.
+// For the others (2 in 10,000) the sign of 127 |p| - h m, h the half between
+// the two candidates, decides: both products are taken as a rounded value and
+// its exact remainder, the values' difference is exact (they are within a
+// factor of 2), and so is the remainders' (at most 508 units of the smaller
+// operand's last place), so the sign is that of the exact difference.
 #include <type_traits>
 
 #include "q4_api_internal.h"
@@ -125,54 +128,78 @@ __device__ __forceinline__ float to_type(float v, const __nv_bfloat16*) {
 // What a row's reduction gives every thread of it.
 struct RowScale {
   float rstd;   // 1 without a norm
-  float inv;    // 127 / m, of the row scaled by 2^100 when tiny
-  float m;      // max |p|, scaled likewise
   float scale;  // the row's scale
+  float up;     // a power of two that brings m near 1 where 127 / m or 127 m could leave fp32's range
+  float m;      // max |p| * up
+  float inv;    // 127 / m, 0 for a row of zeros
   bool bad;     // a value is not finite, or the squares' sum is not
-  bool tiny;    // m below 2^-100: 127 / m could overflow
 };
 
-constexpr float kTiny = 0x1p-100f, kTinyUp = 0x1p100f;
-
-__device__ __forceinline__ RowScale row_scale(uint32_t m_bits, float sum, bool norm, int H, float eps) {
+__device__ __forceinline__ RowScale row_scale(float m, float sum, bool norm, int H, float eps) {
   RowScale s;
-  s.m = __uint_as_float(m_bits);
-  s.bad = m_bits >= 0x7f800000u || (norm && !(sum < INFINITY));
+  s.bad = !(m < INFINITY) || (norm && !(sum < INFINITY));
   s.rstd = norm ? rsqrtf(sum / (float)H + eps) : 1.0f;
-  s.scale = norm ? s.m * s.rstd / 127.0f : s.m / 127.0f;
-  s.tiny = s.m < kTiny;
-  if (s.tiny) s.m *= kTinyUp;
+  s.scale = norm ? m * s.rstd / 127.0f : m / 127.0f;
+  s.up = m < 0x1p-60f ? 0x1p100f : (m > 0x1p60f ? 0x1p-100f : 1.0f);
+  s.m = m * s.up;
   s.inv = s.m > 0.0f ? 127.0f / s.m : 0.0f;
   if (s.bad) {
     s.rstd = __uint_as_float(0x7fc00000u);
     s.scale = s.rstd;
-    s.inv = 0.0f;
-    s.tiny = false;
   }
   return s;
 }
 
-__device__ __noinline__ float code_by_division(float p, float m) {
-  return (float)rint((double)p * 127.0 / (double)m);
+// max of |a| and m, NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float a) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(a)));
+  return d;
 }
 
-// The code of p as the low byte of the result.
-__device__ __forceinline__ uint32_t code_of(float p, float inv, float m) {
+// The rounding of 127 p / m where r = p (127 / m), rounded, is within 1e-4 of
+// a half (see above).
+__device__ __forceinline__ float near_half(float p, float r, float m) {
+  const float a = fabsf(p), lo = floorf(fabsf(r)), h = lo + 0.5f;
+  const float pa = 127.0f * a, pb = h * m;
+  const float d = (pa - pb) + (fmaf(127.0f, a, -pa) - fmaf(h, m, -pb));
+  const float odd = lo - 2.0f * floorf(0.5f * lo);
+  return copysignf(lo + (d > 0.0f ? 1.0f : (d < 0.0f ? 0.0f : odd)), p);
+}
+
+// The codes of p as the low bytes of c.
+template <int VEC>
+__device__ __forceinline__ void codes(const float p[VEC], const RowScale& s, uint32_t c[VEC]) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-  const float r = p * inv;
-  float t = r + kRound;
-  if (fabsf(r - (t - kRound)) > 0.4999f) t = code_by_division(p, m) + kRound;
-  return __float_as_uint(t);
+  float r[VEC], t[VEC], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    r[i] = p[i] * s.inv;
+    t[i] = r[i] + kRound;
+    far = fmaxf(far, fabsf(r[i] - (t[i] - kRound)));
+  }
+  if (far > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (fabsf(r[i] - (t[i] - kRound)) > 0.4999f) t[i] = near_half(p[i], r[i], s.m) + kRound;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) c[i] = __float_as_uint(t[i]);
+}
+
+// p as it stands in registers, brought near 1 (rarely) or to zeros (a bad row).
+template <int VEC>
+__device__ __forceinline__ void ready(float p[VEC], const RowScale& s) {
+  if (s.bad || s.up != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = s.bad ? 0.0f : p[i] * s.up;
+  }
 }
 
 template <int VEC>
 __device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const RowScale& s, int n) {
   uint32_t c[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const float v = s.bad ? 0.0f : (s.tiny ? p[i] * kTinyUp : p[i]);
-    c[i] = code_of(v, s.inv, s.m);
-  }
+  codes<VEC>(p, s, c);
   if constexpr (VEC == 8) {
     if (n >= VEC) {
       uint2 w;
@@ -187,18 +214,34 @@ __device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const
     if (i < n) q[i] = (int8_t)(c[i] & 0xff);
 }
 
-// r (the residual as stored, or x), and p = r * weight.
-template <typename XT, typename RT, bool NORM, int VEC>
-__device__ __forceinline__ void take(const RowArgs& a, long long row, int i, int n, float r[VEC], float p[VEC]) {
+// The row's values r: x, or the residual as it is stored (and here it is).
+template <typename XT, typename RT, int VEC>
+__device__ __forceinline__ void take(const RowArgs& a, long long row, int i, int n, float r[VEC]) {
   load_part<VEC>(reinterpret_cast<const XT*>(a.x) + row * a.ldx + i, r, n);
   if constexpr (!std::is_same<RT, NoRes>::value) {
     float o[VEC];
     load_part<VEC>(reinterpret_cast<const RT*>(a.res) + row * a.ldr + i, o, n);
+    RT* to = reinterpret_cast<RT*>(a.res_out) + row * a.ldro + i;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) r[j] = to_type(r[j] + o[j], (const RT*)nullptr);
+    for (int j = 0; j < VEC; ++j) r[j] += o[j];
+    if constexpr (VEC == 8 && std::is_same<RT, __nv_bfloat16>::value) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = pack_bf16(r[2 * j], r[2 * j + 1]);
+        r[2 * j] = __uint_as_float(w[j] << 16);
+        r[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+      if (n >= VEC)
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        store_part<VEC>(to, r, n);
+    } else {
+      store_part<VEC>(to, r, n);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) r[j] = to_type(r[j], (const RT*)nullptr);
+    }
   }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) p[j] = r[j];
 }
 
 template <int VEC>
@@ -213,27 +256,31 @@ __device__ __forceinline__ void times_weight(const RowArgs& a, int i, int n, flo
   for (int j = 0; j < VEC; ++j) p[j] *= w[j];
 }
 
+__device__ __forceinline__ float warp_max(float m) {
+  // magnitudes compare as their bits do, a NaN above infinity
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
 // Sum and maximum over the CTA's threads, or over a warp's when WARP; every
 // thread gets them (the same bits: both trees are symmetric).
-template <bool WARP>
-__device__ __forceinline__ void reduce(uint32_t& m_bits, float& sum) {
-  m_bits = __reduce_max_sync(0xffffffffu, m_bits);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+template <bool WARP, bool NORM>
+__device__ __forceinline__ void reduce(float& m, float& sum) {
+  m = warp_max(m);
+  if (NORM) sum = warp_sum(sum);
   if constexpr (!WARP) {
-    __shared__ float s_sum[32];
-    __shared__ uint32_t s_max[32];
+    __shared__ float2 part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
-      s_sum[warp] = sum;
-      s_max[warp] = m_bits;
-    }
+    if (lane == 0) part[warp] = make_float2(m, sum);
     __syncthreads();
-    const bool has = lane < (int)(blockDim.x >> 5);
-    sum = has ? s_sum[lane] : 0.0f;
-    m_bits = __reduce_max_sync(0xffffffffu, has ? s_max[lane] : 0u);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float2 v = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float2(0.0f, 0.0f);
+    m = warp_max(v.x);
+    if (NORM) sum = warp_sum(v.y);
   }
 }
 
@@ -246,27 +293,23 @@ __global__ void __launch_bounds__(1024) row_kernel(const __grid_constant__ RowAr
   const long long row = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && row >= a.T) return;
   float p[NV][VEC];
-  float sum = 0.0f;
-  uint32_t m_bits = 0;
+  float sum = 0.0f, m = 0.0f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int i = (me + v * threads) * VEC, n = a.H - i;
     if (n > 0) {
-      float r[VEC];
-      take<XT, RT, NORM, VEC>(a, row, i, n, r, p[v]);
-      if constexpr (!std::is_same<RT, NoRes>::value)
-        store_part<VEC>(reinterpret_cast<RT*>(a.res_out) + row * a.ldro + i, r, n);
+      take<XT, RT, VEC>(a, row, i, n, p[v]);
       if constexpr (NORM) {
-        times_weight<VEC>(a, i, n, p[v]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum = fmaf(r[j], r[j], sum);
+        for (int j = 0; j < VEC; ++j) sum = fmaf(p[v][j], p[v][j], sum);
+        times_weight<VEC>(a, i, n, p[v]);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) m_bits = max(m_bits, __float_as_uint(p[v][j]) & 0x7fffffffu);
+      for (int j = 0; j < VEC; ++j) m = max_abs(m, p[v][j]);
     }
   }
-  reduce<WARP>(m_bits, sum);
-  const RowScale s = row_scale(m_bits, sum, NORM, a.H, a.eps);
+  reduce<WARP, NORM>(m, sum);
+  const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
   if (me == 0 && a.scale) a.scale[row] = s.scale;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -278,7 +321,10 @@ __global__ void __launch_bounds__(1024) row_kernel(const __grid_constant__ RowAr
       for (int j = 0; j < VEC; ++j) o[j] = p[v][j] * s.rstd;
       store_part<VEC>(a.out + row * a.ldo + i, o, n);
     }
-    if (a.q) store_codes<VEC>(a.q + row * a.ldq + i, p[v], s, n);
+    if (a.q) {
+      ready<VEC>(p[v], s);
+      store_codes<VEC>(a.q + row * a.ldq + i, p[v], s, n);
+    }
   }
 }
 
@@ -288,20 +334,18 @@ __global__ void __launch_bounds__(1024) row_kernel(const __grid_constant__ RowAr
 template <typename XT, typename RT, bool NORM>
 __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ RowArgs a) {
   const long long row = blockIdx.x;
-  float sum = 0.0f;
-  uint32_t m_bits = 0;
+  float sum = 0.0f, m = 0.0f;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-    float r[1], p[1];
-    take<XT, RT, NORM, 1>(a, row, i, 1, r, p);
-    if constexpr (!std::is_same<RT, NoRes>::value) reinterpret_cast<RT*>(a.res_out)[row * a.ldro + i] = RT(r[0]);
+    float p[1];
+    take<XT, RT, 1>(a, row, i, 1, p);
     if constexpr (NORM) {
+      sum = fmaf(p[0], p[0], sum);
       times_weight<1>(a, i, 1, p);
-      sum = fmaf(r[0], r[0], sum);
     }
-    m_bits = max(m_bits, __float_as_uint(p[0]) & 0x7fffffffu);
+    m = max_abs(m, p[0]);
   }
-  reduce<false>(m_bits, sum);
-  const RowScale s = row_scale(m_bits, sum, NORM, a.H, a.eps);
+  reduce<false, NORM>(m, sum);
+  const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
   if (threadIdx.x == 0 && a.scale) a.scale[row] = s.scale;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
     float p[1];
@@ -313,7 +357,10 @@ __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ 
       times_weight<1>(a, i, 1, p);
       if (a.out) a.out[row * a.ldo + i] = __float2bfloat16_rn(p[0] * s.rstd);
     }
-    if (a.q) store_codes<1>(a.q + row * a.ldq + i, p, s, 1);
+    if (a.q) {
+      ready<1>(p, s);
+      store_codes<1>(a.q + row * a.ldq + i, p, s, 1);
+    }
   }
 }
 
