@@ -12,14 +12,18 @@
 // the order in which the squares are summed, and the square sum and the
 // maximum come out of one pass over the row with one reduction.
 //
-// Exact quotient: 127 / m and its product with p are each rounded once, so
-// the product is within 127 * 2^-23 < 2e-5 of the quotient; one whose distance
-// from its nearest whole number is below 0.4999 has the quotient's rounding.
-// For the others (2 in 10,000) the sign of 127 |p| - h m, h the half between
-// the two candidates, decides: both products are taken as a rounded value and
-// its exact remainder, the values' difference is exact (they are within a
-// factor of 2), and so is the remainders' (at most 508 units of the smaller
-// operand's last place), so the sign is that of the exact difference.
+// The quotient: 127 / m is held as a rounded value and its remainder, so that
+// p hi + p lo, rounded once, is the quotient's own rounding to fp32.  Adding
+// 1.5 * 2^23 then rounds it to a whole number, ties to even.
+//   - p and m with significands of 16 bits (bf16 rows, times a bf16 weight or
+//     none): a quotient q that is not halfway is at least q / (254 * 65535) from
+//     it, more than the 2^-24 q that a rounding moves it, and a tie is an fp32
+//     value itself, so the codes are right as they are.
+//   - fp32 rows or weights: a value within 2^-16 of a half is settled by the
+//     sign of 127 |p| - h m, h the half.  Both products are taken as a rounded
+//     value and its exact remainder, the values' difference is exact (they are
+//     within a factor of 2), and so is the remainders' (at most 508 units of
+//     the smaller operand's last place), so the sign is the exact one.
 #include <type_traits>
 
 #include "q4_api_internal.h"
@@ -40,6 +44,7 @@ struct RowArgs {
   long long ldx, ldr, ldro, ldo, ldq;
   int T, H;
   int weight_f32;
+  int exact;            // the values' products with the weight have 16-bit significands
   float eps;
 };
 
@@ -131,7 +136,8 @@ struct RowScale {
   float scale;  // the row's scale
   float up;     // a power of two that brings m near 1 where 127 / m or 127 m could leave fp32's range
   float m;      // max |p| * up
-  float inv;    // 127 / m, 0 for a row of zeros
+  float inv;    // 127 / m rounded, 0 for a row of zeros
+  float low;    // what its rounding left
   bool bad;     // a value is not finite, or the squares' sum is not
 };
 
@@ -140,25 +146,55 @@ __device__ __forceinline__ RowScale row_scale(float m, float sum, bool norm, int
   s.bad = !(m < INFINITY) || (norm && !(sum < INFINITY));
   s.rstd = norm ? rsqrtf(sum / (float)H + eps) : 1.0f;
   s.scale = norm ? m * s.rstd / 127.0f : m / 127.0f;
-  s.up = m < 0x1p-60f ? 0x1p100f : (m > 0x1p60f ? 0x1p-100f : 1.0f);
+  s.up = m < 0x1p-60f && m > 0.0f ? 0x1p100f : (m > 0x1p60f ? 0x1p-100f : 1.0f);
   s.m = m * s.up;
   s.inv = s.m > 0.0f ? 127.0f / s.m : 0.0f;
+  s.low = s.m > 0.0f ? fmaf(-s.inv, s.m, 127.0f) / s.m : 0.0f;
   if (s.bad) {
     s.rstd = __uint_as_float(0x7fc00000u);
     s.scale = s.rstd;
+    s.inv = s.low = 0.0f;
   }
   return s;
 }
 
-// max of |a| and m, NaN if either is.
-__device__ __forceinline__ float max_abs(float m, float a) {
+// max(m, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(a)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
   return d;
 }
 
-// The rounding of 127 p / m where r = p (127 / m), rounded, is within 1e-4 of
-// a half (see above).
+// Two fp32 operations an instruction (each rounded as the single one is).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d.v) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void split(F2 d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d.v));
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+// The rounding of 127 p / m where r, the quotient rounded to fp32, is within
+// 2^-16 of a half (see above).
 __device__ __forceinline__ float near_half(float p, float r, float m) {
   const float a = fabsf(p), lo = floorf(fabsf(r)), h = lo + 0.5f;
   const float pa = 127.0f * a, pb = h * m;
@@ -167,21 +203,34 @@ __device__ __forceinline__ float near_half(float p, float r, float m) {
   return copysignf(lo + (d > 0.0f ? 1.0f : (d < 0.0f ? 0.0f : odd)), p);
 }
 
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+
 // The codes of p as the low bytes of c.
 template <int VEC>
-__device__ __forceinline__ void codes(const float p[VEC], const RowScale& s, uint32_t c[VEC]) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-  float r[VEC], t[VEC], far = 0.0f;
+__device__ __forceinline__ void codes(const float p[VEC], const RowScale& s, bool exact, uint32_t c[VEC]) {
+  float r[VEC], t[VEC];
+  if constexpr (VEC == 8) {
+    const F2 inv = f2(s.inv, s.inv), low = f2(s.low, s.low), up = f2(kRound, kRound);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    r[i] = p[i] * s.inv;
-    t[i] = r[i] + kRound;
-    far = fmaxf(far, fabsf(r[i] - (t[i] - kRound)));
+    for (int i = 0; i < 8; i += 2) {
+      const F2 pp = f2(p[i], p[i + 1]), rr = fma(pp, inv, mul(pp, low));
+      split(rr, r[i], r[i + 1]);
+      split(add(rr, up), t[i], t[i + 1]);
+    }
+  } else {
+    r[0] = fmaf(p[0], s.inv, p[0] * s.low);
+    t[0] = r[0] + kRound;
   }
-  if (far > 0.4999f) {
+  if (!exact) {
+    constexpr float kFar = 0.5f - 0x1p-16f;
+    float far = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      if (fabsf(r[i] - (t[i] - kRound)) > 0.4999f) t[i] = near_half(p[i], r[i], s.m) + kRound;
+    for (int i = 0; i < VEC; ++i) far = fmaxf(far, fabsf(r[i] - (t[i] - kRound)));
+    if (far > kFar) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (fabsf(r[i] - (t[i] - kRound)) > kFar) t[i] = near_half(p[i], r[i], s.m) + kRound;
+    }
   }
 #pragma unroll
   for (int i = 0; i < VEC; ++i) c[i] = __float_as_uint(t[i]);
@@ -197,9 +246,9 @@ __device__ __forceinline__ void ready(float p[VEC], const RowScale& s) {
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const RowScale& s, int n) {
+__device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const RowScale& s, bool exact, int n) {
   uint32_t c[VEC];
-  codes<VEC>(p, s, c);
+  codes<VEC>(p, s, exact, c);
   if constexpr (VEC == 8) {
     if (n >= VEC) {
       uint2 w;
@@ -214,33 +263,55 @@ __device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const
     if (i < n) q[i] = (int8_t)(c[i] & 0xff);
 }
 
-// The row's values r: x, or the residual as it is stored (and here it is).
-template <typename XT, typename RT, int VEC>
-__device__ __forceinline__ void take(const RowArgs& a, long long row, int i, int n, float r[VEC]) {
-  load_part<VEC>(reinterpret_cast<const XT*>(a.x) + row * a.ldx + i, r, n);
-  if constexpr (!std::is_same<RT, NoRes>::value) {
-    float o[VEC];
-    load_part<VEC>(reinterpret_cast<const RT*>(a.res) + row * a.ldr + i, o, n);
-    RT* to = reinterpret_cast<RT*>(a.res_out) + row * a.ldro + i;
+// r += o, stored as the residual at `to` and left as it is stored.
+template <typename RT, int VEC>
+__device__ __forceinline__ void add_residual(float r[VEC], const float o[VEC], RT* to, int n) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) r[j] += o[j];
-    if constexpr (VEC == 8 && std::is_same<RT, __nv_bfloat16>::value) {
-      uint32_t w[4];
+  for (int j = 0; j < VEC; ++j) r[j] += o[j];
+  if constexpr (VEC == 8 && std::is_same<RT, __nv_bfloat16>::value) {
+    uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = pack_bf16(r[2 * j], r[2 * j + 1]);
-        r[2 * j] = __uint_as_float(w[j] << 16);
-        r[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-      if (n >= VEC)
-        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
-        store_part<VEC>(to, r, n);
-    } else {
-      store_part<VEC>(to, r, n);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) r[j] = to_type(r[j], (const RT*)nullptr);
+    for (int j = 0; j < 4; ++j) {
+      w[j] = pack_bf16(r[2 * j], r[2 * j + 1]);
+      r[2 * j] = __uint_as_float(w[j] << 16);
+      r[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
+    if (n >= VEC)
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      store_part<VEC>(to, r, n);
+  } else {
+    store_part<VEC>(to, r, n);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) r[j] = to_type(r[j], (const RT*)nullptr);
+  }
+}
+
+// One value of the row: x, or the residual as it is stored (and here it is).
+template <typename XT, typename RT>
+__device__ __forceinline__ void take(const RowArgs& a, long long row, int i, float r[1]) {
+  load_vec<1>(reinterpret_cast<const XT*>(a.x) + row * a.ldx + i, r);
+  if constexpr (!std::is_same<RT, NoRes>::value) {
+    float o[1];
+    load_vec<1>(reinterpret_cast<const RT*>(a.res) + row * a.ldr + i, o);
+    add_residual<RT, 1>(r, o, reinterpret_cast<RT*>(a.res_out) + row * a.ldro + i, 1);
+  }
+}
+
+// A vector of 8 bf16 values, n of them in the row, to a slot: what lies past
+// the row is filled with zeros and not read.
+__device__ __forceinline__ void copy_vector(uint4* to, const __nv_bfloat16* from, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(2 * min(n, 8))
+               : "memory");
+}
+
+__device__ __forceinline__ void unpack(uint4 a, float v[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
@@ -252,8 +323,53 @@ __device__ __forceinline__ void times_weight(const RowArgs& a, int i, int n, flo
     load_part<VEC>(reinterpret_cast<const float*>(a.weight) + i, w, n);
   else
     load_part<VEC>(reinterpret_cast<const __nv_bfloat16*>(a.weight) + i, w, n);
+  if constexpr (VEC == 8) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) p[j] *= w[j];
+    for (int j = 0; j < 8; j += 2) split(mul(f2(p[j], p[j + 1]), f2(w[j], w[j + 1])), p[j], p[j + 1]);
+  } else {
+    p[0] *= w[0];
+  }
+}
+
+// The squares of p added to sum, p times the weight, its largest magnitude
+// into m.
+template <bool NORM, int VEC>
+__device__ __forceinline__ void gather_row(const RowArgs& a, int i, int n, float p[VEC], float& sum, float& m) {
+  if constexpr (VEC == 8) {
+    if constexpr (NORM) {
+      F2 q = mul(f2(p[0], p[1]), f2(p[0], p[1]));
+#pragma unroll
+      for (int j = 2; j < 8; j += 2) q = fma(f2(p[j], p[j + 1]), f2(p[j], p[j + 1]), q);
+      float u, v;
+      split(q, u, v);
+      sum += u + v;
+      times_weight<VEC>(a, i, n, p);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) m = max_abs(m, p[j], p[j + 1]);
+  } else {
+    if constexpr (NORM) {
+      sum = fmaf(p[0], p[0], sum);
+      times_weight<VEC>(a, i, n, p);
+    }
+    m = max_abs(m, p[0], p[0]);
+  }
+}
+
+// What the row's scale makes of p: the bf16 output and the codes.
+template <bool NORM, int VEC>
+__device__ __forceinline__ void put_row(const RowArgs& a, long long row, int i, int n, float p[VEC],
+                                        const RowScale& s) {
+  if (NORM && a.out) {
+    float y[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) y[j] = p[j] * s.rstd;
+    store_part<VEC>(a.out + row * a.ldo + i, y, n);
+  }
+  if (a.q) {
+    ready<VEC>(p, s);
+    store_codes<VEC>(a.q + row * a.ldq + i, p, s, a.exact, n);
+  }
 }
 
 __device__ __forceinline__ float warp_max(float m) {
@@ -269,82 +385,154 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Sum and maximum over the CTA's threads, or over a warp's when WARP; every
 // thread gets them (the same bits: both trees are symmetric).
+// `buf` alternates between a CTA's calls.
 template <bool WARP, bool NORM>
-__device__ __forceinline__ void reduce(float& m, float& sum) {
+__device__ __forceinline__ void reduce(float& m, float& sum, int buf) {
   m = warp_max(m);
   if (NORM) sum = warp_sum(sum);
   if constexpr (!WARP) {
-    __shared__ float2 part[32];
+    __shared__ float2 part[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) part[warp] = make_float2(m, sum);
+    if (lane == 0) part[buf][warp] = make_float2(m, sum);
     __syncthreads();
-    const float2 v = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float2(0.0f, 0.0f);
+    const float2 v = lane < (int)(blockDim.x >> 5) ? part[buf][lane] : make_float2(0.0f, 0.0f);
     m = warp_max(v.x);
     if (NORM) sum = warp_sum(v.y);
   }
 }
 
-// One row a CTA (or a warp), held in registers: NV vectors of VEC values a
-// thread, vector v of thread i at i + v * threads.
-template <typename XT, typename RT, bool NORM, int VEC, int NV, bool WARP>
-__global__ void __launch_bounds__(1024) row_kernel(const __grid_constant__ RowArgs a) {
-  const int threads = WARP ? 32 : blockDim.x;
-  const int me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const long long row = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && row >= a.T) return;
-  float p[NV][VEC];
-  float sum = 0.0f, m = 0.0f;
+// bf16 rows on 16-byte boundaries, THREADS threads a row (32: a warp, four rows
+// a CTA), NV vectors of 8 values a thread, vector v of thread i at
+// 8 (i + v * THREADS).  A CTA takes further rows, and the next one is on its way
+// to shared memory (cp.async, each thread to slots of its own) while this one
+// is reduced and written: the card's bandwidth needs more bytes under way than
+// the registers of a row in work leave room for.  Measured at 8192 rows of
+// 6144, residual and norm: 76 us (5.96 TB/s), rows read into registers with
+// nothing ahead 99 us; two to four rows ahead 75 to 82 us.  4096 rows of 6144
+// to codes alone: 15.8 us against 21.8.
+template <bool RES, bool NORM, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ? 8 : 1024 / THREADS)
+    row_kernel(const __grid_constant__ RowArgs a) {
+  typedef __nv_bfloat16 bf;
+  constexpr bool kWarp = THREADS == 32;
+  constexpr int kCta = kWarp ? 128 : THREADS;
+  extern __shared__ uint4 slots[];  // [NV][x, residual][threads of the CTA]
+  const int me = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  long long row = kWarp ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const long long step = (long long)gridDim.x * (kWarp ? 4 : 1);
+  uint4* const slot = slots + threadIdx.x;
+  auto fetch = [&](long long t) {
+    if (t < a.T) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int i = (me + v * threads) * VEC, n = a.H - i;
-    if (n > 0) {
-      take<XT, RT, VEC>(a, row, i, n, p[v]);
-      if constexpr (NORM) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sum = fmaf(p[v][j], p[v][j], sum);
-        times_weight<VEC>(a, i, n, p[v]);
+      for (int v = 0; v < NV; ++v) {
+        const int i = (me + v * THREADS) * 8, n = a.H - i;
+        if (n > 0) {
+          copy_vector(slot + v * (1 + RES) * kCta, reinterpret_cast<const bf*>(a.x) + t * a.ldx + i, n);
+          if (RES)
+            copy_vector(slot + (v * (1 + RES) + 1) * kCta, reinterpret_cast<const bf*>(a.res) + t * a.ldr + i, n);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) m = max_abs(m, p[v][j]);
     }
-  }
-  reduce<WARP, NORM>(m, sum);
-  const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
-  if (me == 0 && a.scale) a.scale[row] = s.scale;
+  };
+  fetch(row);
+  for (int turn = 0; row < a.T; row += step, turn ^= 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float p[NV][8];
+    float sum = 0.0f, m = 0.0f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int i = (me + v * threads) * VEC, n = a.H - i;
-    if (n <= 0) break;
-    if (NORM && a.out) {
-      float o[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = p[v][j] * s.rstd;
-      store_part<VEC>(a.out + row * a.ldo + i, o, n);
+    for (int v = 0; v < NV; ++v) {
+      const int i = (me + v * THREADS) * 8, n = a.H - i;
+      if (n > 0) {
+        const uint4* x = slot + v * (1 + RES) * kCta;
+        unpack(x[0], p[v]);
+        if constexpr (RES) {
+          float r[8];
+          unpack(x[kCta], r);
+          add_residual<bf, 8>(p[v], r, reinterpret_cast<bf*>(a.res_out) + row * a.ldro + i, n);
+        }
+        gather_row<NORM, 8>(a, i, n, p[v], sum, m);
+      }
     }
-    if (a.q) {
-      ready<VEC>(p[v], s);
-      store_codes<VEC>(a.q + row * a.ldq + i, p[v], s, n);
+    // (in place, a row's results go where only that row was read)
+    fetch(row + step);
+    reduce<kWarp, NORM>(m, sum, turn);
+    const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
+    if (me == 0 && a.scale) a.scale[row] = s.scale;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (me + v * THREADS) * 8, n = a.H - i;
+      if (n > 0) put_row<NORM, 8>(a, row, i, n, p[v], s);
     }
   }
 }
 
-// Rows that do not fit the registers: a CTA a row, two passes over it (the
-// second finds it in L2).  A thread reads in the second pass what it read or
-// wrote in the first, so out may be x and res_out may be res or x.
+// The same straight from memory, NV vectors a thread, a CTA a row: few rows,
+// where one row's latency counts, and rows of fp32.
+template <typename XT, typename RT, bool NORM, int NV>
+__global__ void __launch_bounds__(1024) direct_row_kernel(const __grid_constant__ RowArgs a) {
+  const long long row = blockIdx.x;
+  float p[NV][8];
+  float sum = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = (threadIdx.x + v * blockDim.x) * 8, n = a.H - i;
+    if (n > 0) {
+      load_part<8>(reinterpret_cast<const XT*>(a.x) + row * a.ldx + i, p[v], n);
+      if constexpr (!std::is_same<RT, NoRes>::value) {
+        float r[8];
+        load_part<8>(reinterpret_cast<const RT*>(a.res) + row * a.ldr + i, r, n);
+        add_residual<RT, 8>(p[v], r, reinterpret_cast<RT*>(a.res_out) + row * a.ldro + i, n);
+      }
+      gather_row<NORM, 8>(a, i, n, p[v], sum, m);
+    }
+  }
+  reduce<false, NORM>(m, sum, 0);
+  const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
+  if (threadIdx.x == 0 && a.scale) a.scale[row] = s.scale;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = (threadIdx.x + v * blockDim.x) * 8, n = a.H - i;
+    if (n > 0) put_row<NORM, 8>(a, row, i, n, p[v], s);
+  }
+}
+
+// Rows on other boundaries, value by value: a CTA a row, NV values a thread.
+template <typename XT, typename RT, bool NORM, int NV>
+__global__ void __launch_bounds__(1024) odd_row_kernel(const __grid_constant__ RowArgs a) {
+  const long long row = blockIdx.x;
+  float p[NV][1];
+  float sum = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    if (i < a.H) {
+      take<XT, RT>(a, row, i, p[v]);
+      gather_row<NORM, 1>(a, i, 1, p[v], sum, m);
+    }
+  }
+  reduce<false, NORM>(m, sum, 0);
+  const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
+  if (threadIdx.x == 0 && a.scale) a.scale[row] = s.scale;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    if (i < a.H) put_row<NORM, 1>(a, row, i, 1, p[v], s);
+  }
+}
+
+// Rows that fit neither: a CTA a row, two passes over it (the second finds it
+// in L2).  A thread reads in the second pass what it read or wrote in the
+// first, so out may be x and res_out may be res or x.
 template <typename XT, typename RT, bool NORM>
 __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ RowArgs a) {
   const long long row = blockIdx.x;
   float sum = 0.0f, m = 0.0f;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
     float p[1];
-    take<XT, RT, 1>(a, row, i, 1, p);
-    if constexpr (NORM) {
-      sum = fmaf(p[0], p[0], sum);
-      times_weight<1>(a, i, 1, p);
-    }
-    m = max_abs(m, p[0]);
+    take<XT, RT>(a, row, i, p);
+    gather_row<NORM, 1>(a, i, 1, p, sum, m);
   }
-  reduce<false, NORM>(m, sum);
+  reduce<false, NORM>(m, sum, 0);
   const RowScale s = row_scale(m, sum, NORM, a.H, a.eps);
   if (threadIdx.x == 0 && a.scale) a.scale[row] = s.scale;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
@@ -353,23 +541,32 @@ __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ 
       load_vec<1>(reinterpret_cast<const XT*>(a.x) + row * a.ldx + i, p);
     else
       load_vec<1>(reinterpret_cast<const RT*>(a.res_out) + row * a.ldro + i, p);
-    if constexpr (NORM) {
-      times_weight<1>(a, i, 1, p);
-      if (a.out) a.out[row * a.ldo + i] = __float2bfloat16_rn(p[0] * s.rstd);
-    }
-    if (a.q) {
-      ready<1>(p, s);
-      store_codes<1>(a.q + row * a.ldq + i, p, s, 1);
-    }
+    if constexpr (NORM) times_weight<1>(a, i, 1, p);
+    put_row<NORM, 1>(a, row, i, 1, p, s);
   }
 }
 
-template <typename XT, typename RT, bool NORM, int VEC, int NV>
-cudaError_t launch_rows(const RowArgs& a, int threads, cudaStream_t s) {
-  if (threads <= 32)
-    row_kernel<XT, RT, NORM, VEC, NV, true><<<(unsigned)(((long long)a.T + 3) / 4), 128, 0, s>>>(a);
-  else
-    row_kernel<XT, RT, NORM, VEC, NV, false><<<a.T, threads, 0, s>>>(a);
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 148;
+  return sms;
+}
+
+template <bool RES, bool NORM, int NV, int THREADS>
+cudaError_t launch_rows(const RowArgs& a, cudaStream_t s) {
+  constexpr int cta = THREADS == 32 ? 128 : THREADS, per = cta / THREADS, smem = NV * (1 + RES) * 16 * cta;
+  const auto kernel = row_kernel<RES, NORM, NV, THREADS>;
+  // twice the CTAs that fit an SM (1,024 threads): the second half fills in
+  // where SMs get ahead
+  const long long groups = ((long long)a.T + per - 1) / per, grid = min(groups, 2ll * (1024 / cta) * sm_count());
+  if (smem > 47 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  kernel<<<(unsigned)grid, cta, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -381,29 +578,51 @@ int esize(int type) { return type == MOE_Q4_F32 ? 4 : 2; }
 
 template <typename XT, typename RT, bool NORM>
 int launch(const RowArgs& a, bool vec, cudaStream_t s) {
-  const int V = vec ? 8 : 1;
-  const int units = (a.H + V - 1) / V;
-  // vectors a thread: one while the rows are too few to fill the card (a row's
-  // latency counts), else as many as keep the row's CTA near 256 threads
-  int nv = 1;
-  const int most = 4;
-  while (nv < most && (units > 1024 * nv || (a.T >= 296 && units > 256 * nv))) nv *= 2;
-  cudaError_t e;
-  if (units > 1024 * nv) {
-    row_loop_kernel<XT, RT, NORM><<<a.T, 1024, 0, s>>>(a);
-    e = cudaGetLastError();
-  } else {
-    const int threads = ((units + nv - 1) / nv + 31) / 32 * 32;
-    if (vec)
-      e = nv == 1   ? launch_rows<XT, RT, NORM, 8, 1>(a, threads, s)
-          : nv == 2 ? launch_rows<XT, RT, NORM, 8, 2>(a, threads, s)
-                    : launch_rows<XT, RT, NORM, 8, 4>(a, threads, s);
-    else
-      e = nv == 1   ? launch_rows<XT, RT, NORM, 1, 1>(a, threads, s)
-          : nv == 2 ? launch_rows<XT, RT, NORM, 1, 2>(a, threads, s)
-                    : launch_rows<XT, RT, NORM, 1, 4>(a, threads, s);
+  constexpr bool res = !std::is_same<RT, NoRes>::value;
+  constexpr bool half = std::is_same<XT, __nv_bfloat16>::value && !std::is_same<RT, float>::value;
+  const int units = vec ? (a.H + 7) / 8 : a.H;  // vectors, or values, of a row
+  // two rows an SM and more: the card's bandwidth counts, else a row's latency
+  // (8 rows of 6144: 3.4 us with a thread for each vector, 3.7 by row_kernel)
+  const bool many = a.T >= 296;
+  if (half && vec && many && units <= 4096) {
+    if constexpr (half) {
+      // three or four vectors a thread where the row has them (fewer threads
+      // meet in the reduction, and more rows are in work: 8192 rows of 2048
+      // values 12.3 us with 64 x 4, 15.5 with 256 x 1)
+      const cudaError_t e = units <= 32     ? launch_rows<res, NORM, 1, 32>(a, s)
+                            : units <= 128  ? launch_rows<res, NORM, 4, 32>(a, s)
+                            : units <= 192  ? launch_rows<res, NORM, 3, 64>(a, s)
+                            : units <= 256  ? launch_rows<res, NORM, 4, 64>(a, s)
+                            : units <= 384  ? launch_rows<res, NORM, 3, 128>(a, s)
+                            : units <= 512  ? launch_rows<res, NORM, 4, 128>(a, s)
+                            : units <= 768  ? launch_rows<res, NORM, 3, 256>(a, s)
+                            : units <= 1024 ? launch_rows<res, NORM, 4, 256>(a, s)
+                                            : launch_rows<res, NORM, 4, 1024>(a, s);
+      return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+    }
   }
-  return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+  if (units > 4096) {
+    row_loop_kernel<XT, RT, NORM><<<a.T, 1024, 0, s>>>(a);
+  } else {
+    // fp32 (twice the bytes a vector, so enough are under way): 8192 rows of
+    // 6144 with an fp32 residual 113 us (6.7 TB/s) with two vectors a thread,
+    // 118 with four, 151 with one
+    const int nv = units > 2048 || (!vec && many && units > 512) ? 4 : (units > 1024 || (many && units > 256) ? 2 : 1);
+    const int threads = ((units + nv - 1) / nv + 31) / 32 * 32;
+    if (vec && nv == 1)
+      direct_row_kernel<XT, RT, NORM, 1><<<a.T, threads, 0, s>>>(a);
+    else if (vec && nv == 2)
+      direct_row_kernel<XT, RT, NORM, 2><<<a.T, threads, 0, s>>>(a);
+    else if (vec)
+      direct_row_kernel<XT, RT, NORM, 4><<<a.T, threads, 0, s>>>(a);
+    else if (nv == 1)
+      odd_row_kernel<XT, RT, NORM, 1><<<a.T, threads, 0, s>>>(a);
+    else if (nv == 2)
+      odd_row_kernel<XT, RT, NORM, 2><<<a.T, threads, 0, s>>>(a);
+    else
+      odd_row_kernel<XT, RT, NORM, 4><<<a.T, threads, 0, s>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
 bool row_type(int t) { return t == MOE_Q4_BF16 || t == MOE_Q4_F32; }
@@ -424,7 +643,7 @@ extern "C" int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T
   RowArgs a = {};
   a.x = x, a.ldx = ldx;
   a.q = q, a.ldq = ldq, a.scale = scale;
-  a.T = T, a.H = K;
+  a.T = T, a.H = K, a.exact = x_type == MOE_Q4_BF16;
   const bool vec = aligned(x, ldx, esize(x_type), 16) && aligned(q, ldq, 1, 8);
   const cudaStream_t s = (cudaStream_t)stream;
   return x_type == MOE_Q4_F32 ? launch<float, NoRes, false>(a, vec, s)
@@ -455,6 +674,7 @@ extern "C" int moe_q4_add_norm(const void* x, int x_type, long long ldx, const v
   a.out = (__nv_bfloat16*)out, a.ldo = ldo;
   a.q = q, a.ldq = ldq, a.scale = scale;
   a.T = T, a.H = H, a.eps = eps;
+  a.exact = (residual ? residual_type : x_type) == MOE_Q4_BF16 && (!weight || weight_type == MOE_Q4_BF16);
   bool vec = aligned(x, ldx, esize(x_type), 16) && aligned(weight, 0, 1, 16) && (!out || aligned(out, ldo, 2, 16)) &&
              (!q || aligned(q, ldq, 1, 8));
   if (residual)
