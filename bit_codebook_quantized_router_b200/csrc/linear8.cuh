@@ -17,6 +17,8 @@ struct LinArgs {
   long long ldx, ldw, ldo;
   int T, N, K;
   int out_f32;
+  int chained;           // launched behind a kernel of the same call that lets it start early: the weights
+                         // may be read at once, x and xs after griddepcontrol.wait
 };
 
 // The one place that turns a sum into a value: the same bits in every kernel.
@@ -35,4 +37,4 @@ __device__ __forceinline__ void store_out(const LinArgs& a, long long t, int n, 
 // tokens (K split over a cluster) and for many (CTA pairs).
 int q4_launch_linear_mid(const q4::LinArgs& a, bool gated, cudaStream_t s);
 int q4_launch_linear_wide(const q4::LinArgs& a, bool gated, cudaStream_t s);
-constexpr int kLinearMidTokens = 256;  // the most that q4_launch_linear_mid takes
+constexpr int kLinearMidTokens = 64;  // the most that q4_launch_linear_mid takes

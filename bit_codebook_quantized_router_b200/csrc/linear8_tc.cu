@@ -1,12 +1,12 @@
 // Int8 products on the 5th-generation tensor cores (tcgen05, kind::i8, int32
 // accumulators in TMEM), for moderate and large numbers of tokens.
 //
-// mid_kernel, up to 256 tokens: the weights' bytes bound it.  The MMA's M is
-// 128 weight rows and its N all the tokens, so each weight is read once; K is
-// split over the CTAs of a cluster so that every SM streams weights.  The
-// partial sums are int32, so adding them is exact in any order: each CTA
-// sends the columns that another owns to that CTA's shared memory, and each
-// finishes its own columns.  No workspace and one launch.
+// mid_kernel, up to 64 tokens: the weights' bytes bound it.  The MMA's M is 128
+// weight rows and its N all the tokens, so each weight is read once; K is split
+// over the CTAs of a cluster so that every SM streams weights.  The partial
+// sums are int32, so adding them is exact in any order: each CTA sends the
+// columns that another owns to that CTA's shared memory, and each finishes its
+// own columns.  No workspace and one launch.
 //
 // wide_kernel, more tokens: pairs of CTAs (cta_group::2) multiply 256 tokens
 // by 256 weight rows, each CTA holding 128 rows of both operands, so a pair
@@ -38,6 +38,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSmemExtra = 2048;       // alignment and barriers
+constexpr int kMidStages = 8;
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -58,24 +59,25 @@ __device__ __forceinline__ void give_up(int32_t* status, uint64_t* full, int sta
 
 struct MidPlan {
   int bn;       // tokens, rounded up to 16
+  int own;      // columns that a CTA of the cluster finishes (a multiple of 8)
   int stages;   // ring stages
   int ksteps;   // k-steps of 128 in K
 };
 
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads)
     mid_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ MidPlan p,
                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint64_t full[kMidStages], empty[kMidStages], acc_full[1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  __shared__ float s_xs[kLinearMidTokens];
+  volatile int* abort_flag = &abort_word;
   uint8_t* smem = align1024(smem_raw);
   const int S = p.stages, b_tile = p.bn * kBK;
   uint8_t* sA = smem;              // [S][128][128 B] weights
   uint8_t* sB = sA + S * kTile;    // [S][bn][128 B] tokens
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * b_tile);
-  uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = gridDim.y, rank = blockIdx.y;  // the cluster's CTAs share blockIdx.x
@@ -84,6 +86,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k_hi = (int)((long long)p.ksteps * (rank + 1) / splits);
   uint32_t cols = 32;
   while (cols < (uint32_t)p.bn) cols *= 2;
+  auto load_w = [&](int ks, int s) {
+    mbar_arrive_expect_tx(&full[s], kTile + b_tile);
+    tma_load_2d(sA + s * kTile, &tm_w, &full[s], ks * kBK, n0);
+    if (GATED) tma_load_2d(sA + s * kTile + kTile / 2, &tm_w, &full[s], ks * kBK, a.N + n0);
+  };
+  auto load_x = [&](int ks, int s) { tma_load_2d(sB + s * b_tile, &tm_x, &full[s], ks * kBK, 0); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -93,42 +101,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(acc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&tm_x);
-    prefetch_tmap(&tm_w);
+    // the ring's first loads, before anything is set up beside them; the
+    // weights' before the kernel in front is done with the tokens
+    for (int i = 0; i < S && k_lo + i < k_hi; ++i) load_w(k_lo + i, i);
+    pdl_wait();
+    for (int i = 0; i < S && k_lo + i < k_hi; ++i) load_x(k_lo + i, i);
   }
+  __syncwarp();
+  pdl_wait();
+  pdl_trigger();
   if (warp == 1) {
-    tmem_alloc(tmem_slot, cols);
+    tmem_alloc(&tmem_slot, cols);
     tmem_relinquish();
+  }
+  // what the results are scaled with, while the sums are made
+  const int c_lo = rank * p.own, c_n = min(p.own, a.T - c_lo);
+  const int et = threadIdx.x - 32 * kEpiWarp0;  // epilogue thread: one weight row, every second (fourth) column
+  constexpr int kRows = GATED ? 64 : 128;
+  const int n = n0 + (et & (kRows - 1));
+  float wscale = 0.0f, uscale = 0.0f, bias = 0.0f;
+  if (et >= 0) {
+    if (n < a.N) {
+      wscale = a.ws[n];
+      if (GATED) uscale = a.ws[a.N + n];
+      if (!GATED && a.bias) bias = a.bias[n];
+    }
+    if (et < c_n) s_xs[et] = a.xs[c_lo + et];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = tmem_slot;
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
-      for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
+      int it = S;
+      for (int ks = k_lo + S; ks < k_hi; ++ks, ++it) {
         const int s = it % S;
         if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort_flag, kWaitNs)) break;
-        mbar_arrive_expect_tx(&full[s], kTile + b_tile);
-        if (GATED) {
-          tma_load_2d(sA + s * kTile, &tm_w, &full[s], ks * kBK, n0);
-          tma_load_2d(sA + s * kTile + kTile / 2, &tm_w, &full[s], ks * kBK, a.N + n0);
-        } else {
-          tma_load_2d(sA + s * kTile, &tm_w, &full[s], ks * kBK, n0);
-        }
-        tma_load_2d(sB + s * b_tile, &tm_x, &full[s], ks * kBK, 0);
+        load_w(ks, s);
+        load_x(ks, s);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = umma_idesc_s8(128, p.bn);
       int it = 0;
-      bool ok = true;
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
         const int s = it % S;
-        if (!(ok = mbar_wait(&full[s], (it / S) & 1, abort_flag, kWaitNs))) break;
+        if (!mbar_wait(&full[s], (it / S) & 1, abort_flag, kWaitNs)) break;
         tc_fence_after();
         const uint64_t da = umma_desc_sw128(smem_u32(sA + s * kTile));
         const uint64_t db = umma_desc_sw128(smem_u32(sB + s * b_tile));
@@ -142,54 +163,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  // every copy has been read by an MMA and every MMA is done (or the wait for
-  // it was given up): the ring's memory is free, here and, past the barrier,
-  // in every CTA of the cluster
+  // every copy has been read by an MMA and every MMA is done, or a wait was
+  // given up: the ring's memory is free here
   if (threadIdx.x == 0 && *abort_flag) give_up(a.status, full, S);
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-
-  // send: columns [own * r, own * (r + 1)) to CTA r as [src][column][128]
-  const int own = (p.bn + splits - 1) / splits;
-  const uint32_t inbox = smem_u32(smem) + (uint32_t)rank * own * 512;
+  __syncwarp();
+  if (splits > 1) {
+    cluster_arrive();  // and past the barrier in every CTA of the cluster
+    cluster_wait();
+  }
+  // send: columns [own * r, own * (r + 1)) to CTA r as [src][column][128 rows],
+  // a warp 128 consecutive bytes at a time (16 bytes a lane at a row's pitch
+  // measured slower, 17.1 against 14.6 us at 64 tokens and 6144 x 6144, and so
+  // did bulk copies of what was gathered here first, 15.6)
   tc_fence_after();
   if (warp >= kEpiWarp0) {
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, row = quad * 32 + lane;
     const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16);
-    for (int c0 = half * 8; c0 < p.bn; c0 += 16) {
-      uint32_t v[8];
-      tmem_ld8_nowait(tb + c0, v);
+    const uint32_t inbox = smem_u32(smem) + (rank * p.own * 128 + row) * 4;
+    for (int c0 = half * 16; c0 < p.bn; c0 += 32) {
+      uint32_t v[16];
+      tmem_ld16_nowait(tb + c0, v);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = c0 + j, to = c / own;
-        cluster_st32(cluster_addr(inbox + ((c - to * own) * 128 + row) * 4, to), (int)v[j]);
+      for (int h = 0; h < 16; h += 8) {
+        const int to = (c0 + h) / p.own;
+        const uint32_t at = cluster_addr(inbox + (c0 + h - to * p.own) * 512, to);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cluster_st32(at + j * 512, v[h + j]);
       }
     }
   }
   tc_fence_before();
-  cluster_arrive();
-  cluster_wait();
+  if (splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
 
   // finish this CTA's columns
-  const int* box = reinterpret_cast<const int*>(smem);
-  constexpr int kRows = GATED ? 64 : 128;
-  const int c_lo = rank * own, c_n = min(own, a.T - c_lo);
-  for (int i = threadIdx.x; i < c_n * kRows; i += kThreads) {
-    const int c = i / kRows, r = i % kRows, n = n0 + r, t = c_lo + c;
-    if (n >= a.N) continue;
-    int v = 0, u = 0;
-    for (int src = 0; src < splits; ++src) {
-      v += box[(src * own + c) * 128 + r];
-      if (GATED) u += box[(src * own + c) * 128 + 64 + r];
+  if (et >= 0 && n < a.N) {
+    const int* box = reinterpret_cast<const int*>(smem) + (et & (kRows - 1));
+#pragma unroll 4
+    for (int c = et / kRows; c < c_n; c += 32 * kEpiWarps / kRows) {
+      int v = 0, u = 0;
+      for (int src = 0; src < splits; ++src) {
+        v += box[(src * p.own + c) * 128];
+        if (GATED) u += box[(src * p.own + c) * 128 + 64];
+      }
+      const float xs = s_xs[c];
+      float y = scaled(v, xs, wscale);
+      if (GATED)
+        y = silu_mul(y, scaled(u, xs, uscale));
+      else if (a.bias)
+        y += bias;
+      store_out(a, c_lo + c, n, y);
     }
-    float y = scaled(v, a.xs[t], a.ws[n]);
-    if (GATED)
-      y = silu_mul(y, scaled(u, a.xs[t], a.ws[a.N + n]));
-    else if (a.bias)
-      y += a.bias[n];
-    store_out(a, t, n, y);
   }
   if (warp == 1) {
     __syncwarp();
@@ -201,9 +230,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- many tokens ----------------------------------------------------------------
 
 constexpr int kWideStages = 6;
-constexpr int kWideSmem = kWideStages * 2 * kTile + kSmemExtra;
+constexpr int kWideRow = 17;  // floats of a staged row of 16
+constexpr int kWideSmem = kWideStages * 2 * kTile + kSmemExtra + 2 * 512 * 4 + kEpiWarps * 32 * kWideRow * 4;
 
-template <bool GATED>
+// How the output's rows can be written: 32 bytes at a time, 16, or as they come.
+__device__ __forceinline__ int out_align(const LinArgs& a) {
+  const unsigned long long es = a.out_f32 ? 4 : 2, b = (uintptr_t)a.out | (a.ldo * es);
+  return b % 32 == 0 ? 32 : (b % 16 == 0 ? 16 : 1);
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t w[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 16 values of row t from column n, one row a lane (t >= a.T: nothing).
+// A row's values leave in whole sectors where its alignment allows; else they
+// go through shared memory, so that lanes write along the rows.
+__device__ __forceinline__ void store_row16(const LinArgs& a, int align, float* stage, long long t, int n,
+                                            const float y[16]) {
+  const int lane = threadIdx.x & 31;
+  if (align > 1 && n + 16 <= a.N) {
+    if (t >= a.T) return;
+    uint32_t w[16];
+    int words;
+    char* p;
+    if (a.out_f32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(y[j]);
+      p = reinterpret_cast<char*>(reinterpret_cast<float*>(a.out) + t * a.ldo + n);
+      words = 16;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      p = reinterpret_cast<char*>(reinterpret_cast<__nv_bfloat16*>(a.out) + t * a.ldo + n);
+      words = 8;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 8) {
+      if (j >= words) break;
+      if (align == 32) {
+        store32(p + 4 * j, w + j);
+      } else {
+        reinterpret_cast<uint4*>(p + 4 * j)[0] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        reinterpret_cast<uint4*>(p + 4 * j)[1] = make_uint4(w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) stage[lane * kWideRow + j] = y[j];
+  __syncwarp();
+  const int c = lane & 15;
+  if (n + c < a.N)
+#pragma unroll 8
+    for (int r = lane >> 4; r < 32; r += 2)
+      if (t - lane + r < a.T) store_out(a, t - lane + r, n + c, stage[r * kWideRow + c]);
+  __syncwarp();
+}
+
+template <bool GATED, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     wide_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ CUtensorMap tm_x,
                 const __grid_constant__ CUtensorMap tm_w) {
@@ -217,6 +307,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;        // [2], the even CTA's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_scale = reinterpret_cast<float*>(sB + kWideStages * kTile + 512);  // [2][256] the columns' scales
+  float* s_bias = s_scale + 512;                                              // [2][256] and biases
+  float* s_rows = s_bias + 512;                                               // [epilogue warps][32][kWideRow]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -234,16 +327,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tm_x);
     prefetch_tmap(&tm_w);
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 2 * BN);
   tc_fence_before();
   __syncthreads();
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
 
   const int m_tiles = (a.T + 255) / 256;
-  constexpr int kBN = GATED ? 128 : 256;  // output columns of a tile
+  constexpr int kBN = GATED ? BN / 2 : BN;  // output columns of a tile
   const int n_tiles = (a.N + kBN - 1) / kBN;
   const int total = m_tiles * n_tiles;
   const int ksteps = (a.K + kBK - 1) / kBK;
@@ -252,18 +346,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
-      bool ok = true;
+      bool ok = true, filled = false;
       for (int tile = first; tile < total && ok; tile += step) {
         const int m = tile % m_tiles, n = tile / m_tiles;
         const int ya = m * 256 + rank * 128;
-        const int yb = GATED ? rank * a.N + n * 128 : n * 256 + rank * 128;
+        const int yb = GATED ? rank * a.N + n * kBN : n * BN + rank * (BN / 2);
         for (int ks = 0; ks < ksteps; ++ks, ++it) {
           const int s = it % kWideStages;
           if (!(ok = mbar_wait(&empty[s], ((it / kWideStages) & 1) ^ 1, abort_flag, kWaitNs))) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kTile);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kTile + BN / 2 * kBK));
           const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
-          tma_load_2d_pair(sA + s * kTile, &tm_x, bar, ks * kBK, ya);
           tma_load_2d_pair(sB + s * kTile, &tm_w, bar, ks * kBK, yb);
+          // the ring's first weights are asked for before the kernel in front
+          // is done with the tokens
+          if (!filled) {
+            if ((int)it + 1 < min(kWideStages, ksteps)) continue;
+            pdl_wait();
+            for (int i = 0; i < ks; ++i)
+              tma_load_2d_pair(sA + i * kTile, &tm_x, cluster_addr(smem_u32(&full[i]), 0), i * kBK, ya);
+            filled = true;
+          }
+          tma_load_2d_pair(sA + s * kTile, &tm_x, bar, ks * kBK, ya);
         }
       }
       // the last MMAs' arrivals at this CTA's barriers, so that none comes after its end
@@ -272,14 +375,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = umma_idesc_s8(256, 256);
+      const uint32_t idesc = umma_idesc_s8(256, BN);
       uint32_t it = 0, use = 0;
       bool ok = true;
       for (int tile = first; tile < total && ok; tile += step, ++use) {
         const int buf = use & 1;
         if (!(ok = mbar_wait(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, kWaitNs))) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * 256;
+        const uint32_t d = tmem + buf * BN;
         for (int ks = 0; ks < ksteps; ++ks, ++it) {
           const int s = it % kWideStages;
           if (!(ok = mbar_wait(&full[s], (it / kWideStages) & 1, abort_flag, kWaitNs))) break;
@@ -295,61 +398,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
-    const int es = a.out_f32 ? 4 : 2;
-    const bool vec = ((uintptr_t)a.out & 15) == 0 && (a.ldo * es) % 16 == 0;
+    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, e = threadIdx.x - 32 * kEpiWarp0;
+    const int align = out_align(a);
+    pdl_wait();
+    float* stage = s_rows + (warp - kEpiWarp0) * 32 * kWideRow;
     uint32_t use = 0;
     for (int tile = first; tile < total; tile += step, ++use) {
       const int m = tile % m_tiles, n0 = tile / m_tiles * kBN;
       const int buf = use & 1;
-      if (!mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs)) break;
-      tc_fence_after();
+      // the columns' scales, while the tile is multiplied (a buffer is written
+      // again two tiles later, past the barrier of the tile between)
+      {
+        const int n = n0 + (e & (kBN - 1));
+        float* sc = s_scale + buf * 256;
+        if (e < BN) sc[e] = n < a.N ? a.ws[GATED && e >= kBN ? a.N + n : n] : 0.0f;
+        if (!GATED && e < BN) s_bias[buf * 256 + e] = a.bias && n < a.N ? a.bias[n] : 0.0f;
+      }
       const long long t = (long long)m * 256 + rank * 128 + quad * 32 + lane;
       const float xs = t < a.T ? a.xs[t] : 0.0f;
-      const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + buf * 256;
-      for (int c0 = half * (kBN / 2); c0 < (half + 1) * (kBN / 2); c0 += 16) {
-        uint32_t v[16], u[16];
-        __syncwarp();  // (rows past T skip the stores below)
-        tmem_ld16_nowait(tb + c0, v);
-        if (GATED) tmem_ld16_nowait(tb + 128 + c0, u);
+      named_bar(1, 32 * kEpiWarps);
+      if (!mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
+      constexpr int kCols = kBN / 2;  // of this warp
+      uint32_t v[2][16], u[2][16];
+      auto load = [&](int i) {
+        const int c = half * kCols + i * 16;
+        tmem_ld16_nowait(tb + c, v[i & 1]);
+        if (GATED) tmem_ld16_nowait(tb + kBN + c, u[i & 1]);
+      };
+      load(0);
+#pragma unroll
+      for (int i = 0; i < kCols / 16; ++i) {
         tmem_wait_ld();
-        const int n = n0 + c0;
+        if (i + 1 < kCols / 16) {
+          load(i + 1);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[buf]), 0));
+        }
+        const int c = half * kCols + i * 16;
+        const float* sc = s_scale + buf * 256 + c;
+        const float* sb = s_bias + buf * 256 + c;
         float y[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int nj = min(n + j, a.N - 1);
-          y[j] = scaled((int)v[j], xs, a.ws[nj]);
+          y[j] = scaled((int)v[i & 1][j], xs, sc[j]);
           if (GATED)
-            y[j] = silu_mul(y[j], scaled((int)u[j], xs, a.ws[a.N + nj]));
+            y[j] = silu_mul(y[j], scaled((int)u[i & 1][j], xs, sc[kBN + j]));
           else if (a.bias)
-            y[j] += a.bias[nj];
+            y[j] += sb[j];
         }
-        if (t >= a.T) {
-        } else if (vec && n + 16 <= a.N) {
-          if (a.out_f32) {
-            float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + t * a.ldo + n);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-          } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-              w[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + t * a.ldo + n);
-            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (n + j < a.N) store_out(a, t, n + j, y[j]);
-        }
+        store_row16(a, align, stage, t, n0 + c, y);
+        __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[buf]), 0));
     }
   }
 
@@ -361,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * BN);
   }
 }
 
@@ -408,55 +511,79 @@ int launch_mid(const LinArgs& a, cudaStream_t s) {
   p.bn = (a.T + 15) / 16 * 16;
   p.ksteps = (a.K + kBK - 1) / kBK;
   const int tiles = GATED ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  // K split until every SM has a CTA, at most a portable cluster of 8, and two k-steps each
-  int splits = 1;
   const int sms = sm_count();
-  while (splits < 8 && tiles * (splits + 1) <= sms && p.ksteps >= 2 * (splits + 1)) ++splits;
-  const int stage = kTile + p.bn * kBK;
-  p.stages = (kSmemLimit - kSmemExtra) / stage;
-  if (p.stages > 10) p.stages = 10;
-  const int most = (p.ksteps + splits - 1) / splits;
-  // the ring is also the inbox of the partial sums, 512 bytes a column and source
-  const int box = splits * ((p.bn + splits - 1) / splits) * 512;
-  if (p.stages > most) p.stages = most;
-  if (p.stages * stage < box) p.stages = (box + stage - 1) / stage;
-  const int smem = p.stages * stage + kSmemExtra;
-  if (smem > kSmemLimit) return MOE_Q4_ECUDA;
+  // K split in two, four or eight while the CTAs fit the card at two an SM
+  // (clusters leave an eighth of them unused) and keep two k-steps
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 2 * sms * 7 / 8 && p.ksteps >= 4 * splits) splits *= 2;
+  p.own = (p.bn / 8 + splits - 1) / splits * 8;
+  const int stage = kTile + p.bn * kBK, most = (p.ksteps + splits - 1) / splits, box = splits * p.own * 512;
+  p.stages = min(min(most, kMidStages), 108 * 1024 / stage);
+  if (p.stages * stage < box) p.stages = (box + stage - 1) / stage;  // (the ring takes the partial sums)
+  const int smem = p.stages * stage + 1024;
   CUtensorMap tx, tw;
   if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, p.bn) ||
       !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, GATED ? 64 : 128))
     return MOE_Q4_ECUDA;
-  if (cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
+  if (cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return MOE_Q4_ECUDA;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = splits;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.chained ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, mid_kernel<GATED>, a, p, tx, tw) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+}
+
+template <bool GATED, int BN>
+int launch_wide(const LinArgs& a, cudaStream_t s) {
+  constexpr int cols = GATED ? BN / 2 : BN;
+  const long long tiles = (((long long)a.T + 255) / 256) * ((a.N + cols - 1) / cols);
+  if (tiles > 0x3fffffff) return MOE_Q4_ENOTSUP;
+  CUtensorMap tx, tw;
+  if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, 128) ||
+      !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, BN / 2))
+    return MOE_Q4_ECUDA;
+  const auto kernel = wide_kernel<GATED, BN>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
+    return MOE_Q4_ECUDA;
+  const int pairs = sm_count() / 2;
+  const int grid = 2 * (int)(tiles < pairs ? tiles : pairs);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWideSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.chained;
+  return cudaLaunchKernelEx(&cfg, kernel, a, tx, tw) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
 template <bool GATED>
 int launch_wide(const LinArgs& a, cudaStream_t s) {
-  const long long tiles = (((long long)a.T + 255) / 256) * ((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
-  if (tiles > 0x3fffffff) return MOE_Q4_ENOTSUP;
-  CUtensorMap tx, tw;
-  if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, 128) ||
-      !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, 128))
-    return MOE_Q4_ECUDA;
-  if (cudaFuncSetAttribute(wide_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
-    return MOE_Q4_ECUDA;
-  const int pairs = sm_count() / 2;
-  const int grid = 2 * (int)(tiles < pairs ? tiles : pairs);
-  wide_kernel<GATED><<<grid, kThreads, kWideSmem, s>>>(a, tx, tw);
-  return cudaGetLastError() == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+  // A k-step takes 0.26 to 0.28 us whatever the tile's width (the MMA's 256 rows
+  // bound it), so tiles are wide; narrower ones are for products whose tiles
+  // leave SMs idle: each then writes fewer results (T = 256, N = 6144,
+  // K = 2048: 12.6 us with 256 columns, 11.9 with 128, 14.8 with 64 in two
+  // turns; N = K = 512: 8.0, 6.6 and 5.8).
+  const long long m = (a.T + 255) / 256, pairs = sm_count() / 2, n = GATED ? 2ll * a.N : a.N;
+  if (m * ((n + 63) / 64) <= pairs) return launch_wide<GATED, 64>(a, s);
+  if (m * ((n + 127) / 128) <= pairs) return launch_wide<GATED, 128>(a, s);
+  return launch_wide<GATED, 256>(a, s);
 }
 
 }  // namespace

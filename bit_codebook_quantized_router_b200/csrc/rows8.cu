@@ -12,22 +12,10 @@
 // the order in which the squares are summed, and the square sum and the
 // maximum come out of one pass over the row with one reduction.
 //
-// The quotient: 127 / m is held as a rounded value and its remainder, so that
-// p hi + p lo, rounded once, is the quotient's own rounding to fp32.  Adding
-// 1.5 * 2^23 then rounds it to a whole number, ties to even.
-//   - p and m with significands of 16 bits (bf16 rows, times a bf16 weight or
-//     none): a quotient q that is not halfway is at least q / (254 * 65535) from
-//     it, more than the 2^-24 q that a rounding moves it, and a tie is an fp32
-//     value itself, so the codes are right as they are.
-//   - fp32 rows or weights: a value within 2^-16 of a half is settled by the
-//     sign of 127 |p| - h m, h the half.  Both products are taken as a rounded
-//     value and its exact remainder, the values' difference is exact (they are
-//     within a factor of 2), and so is the remainders' (at most 508 units of
-//     the smaller operand's last place), so the sign is the exact one.
+// (rows8.cuh has the arithmetic.)
 #include <type_traits>
 
-#include "q4_api_internal.h"
-#include "q4_common.cuh"
+#include "rows8.cuh"
 
 namespace q4 {
 
@@ -43,10 +31,35 @@ struct RowArgs {
   float* scale;
   long long ldx, ldr, ldro, ldo, ldq;
   int T, H;
+  int chained;          // launched behind a kernel of the same call that lets it start early
   int weight_f32;
   int exact;            // the values' products with the weight have 16-bit significands
   float eps;
 };
+
+// In a chain the next kernel may start at once (it waits itself before it
+// reads this one's rows), and this one waits for the rows it reads.
+__device__ __forceinline__ void begin(const RowArgs& a) {
+  if (a.chained) {
+    pdl_trigger();
+    pdl_wait();
+  }
+}
+
+template <typename K>
+cudaError_t start(K kernel, const RowArgs& a, long long grid, int threads, int smem, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.chained;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 
 struct NoRes {};  // residual type of a call without one
 
@@ -130,131 +143,13 @@ __device__ __forceinline__ float to_type(float v, const __nv_bfloat16*) {
   return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// What a row's reduction gives every thread of it.
-struct RowScale {
-  float rstd;   // 1 without a norm
-  float scale;  // the row's scale
-  float up;     // a power of two that brings m near 1 where 127 / m or 127 m could leave fp32's range
-  float m;      // max |p| * up
-  float inv;    // 127 / m rounded, 0 for a row of zeros
-  float low;    // what its rounding left
-  bool bad;     // a value is not finite, or the squares' sum is not
-};
-
-__device__ __forceinline__ RowScale row_scale(float m, float sum, bool norm, int H, float eps) {
-  RowScale s;
-  s.bad = !(m < INFINITY) || (norm && !(sum < INFINITY));
-  s.rstd = norm ? rsqrtf(sum / (float)H + eps) : 1.0f;
-  s.scale = norm ? m * s.rstd / 127.0f : m / 127.0f;
-  s.up = m < 0x1p-60f && m > 0.0f ? 0x1p100f : (m > 0x1p60f ? 0x1p-100f : 1.0f);
-  s.m = m * s.up;
-  s.inv = s.m > 0.0f ? 127.0f / s.m : 0.0f;
-  s.low = s.m > 0.0f ? fmaf(-s.inv, s.m, 127.0f) / s.m : 0.0f;
-  if (s.bad) {
-    s.rstd = __uint_as_float(0x7fc00000u);
-    s.scale = s.rstd;
-    s.inv = s.low = 0.0f;
-  }
-  return s;
-}
-
-// max(m, |a|, |b|), NaN if any is.
-__device__ __forceinline__ float max_abs(float m, float a, float b) {
-  float d;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
-  return d;
-}
-
-// Two fp32 operations an instruction (each rounded as the single one is).
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d.v) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void split(F2 d, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d.v));
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return d;
-}
-
-// The rounding of 127 p / m where r, the quotient rounded to fp32, is within
-// 2^-16 of a half (see above).
-__device__ __forceinline__ float near_half(float p, float r, float m) {
-  const float a = fabsf(p), lo = floorf(fabsf(r)), h = lo + 0.5f;
-  const float pa = 127.0f * a, pb = h * m;
-  const float d = (pa - pb) + (fmaf(127.0f, a, -pa) - fmaf(h, m, -pb));
-  const float odd = lo - 2.0f * floorf(0.5f * lo);
-  return copysignf(lo + (d > 0.0f ? 1.0f : (d < 0.0f ? 0.0f : odd)), p);
-}
-
-constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-
-// The codes of p as the low bytes of c.
-template <int VEC>
-__device__ __forceinline__ void codes(const float p[VEC], const RowScale& s, bool exact, uint32_t c[VEC]) {
-  float r[VEC], t[VEC];
-  if constexpr (VEC == 8) {
-    const F2 inv = f2(s.inv, s.inv), low = f2(s.low, s.low), up = f2(kRound, kRound);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const F2 pp = f2(p[i], p[i + 1]), rr = fma(pp, inv, mul(pp, low));
-      split(rr, r[i], r[i + 1]);
-      split(add(rr, up), t[i], t[i + 1]);
-    }
-  } else {
-    r[0] = fmaf(p[0], s.inv, p[0] * s.low);
-    t[0] = r[0] + kRound;
-  }
-  if (!exact) {
-    constexpr float kFar = 0.5f - 0x1p-16f;
-    float far = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) far = fmaxf(far, fabsf(r[i] - (t[i] - kRound)));
-    if (far > kFar) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (fabsf(r[i] - (t[i] - kRound)) > kFar) t[i] = near_half(p[i], r[i], s.m) + kRound;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) c[i] = __float_as_uint(t[i]);
-}
-
-// p as it stands in registers, brought near 1 (rarely) or to zeros (a bad row).
-template <int VEC>
-__device__ __forceinline__ void ready(float p[VEC], const RowScale& s) {
-  if (s.bad || s.up != 1.0f) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = s.bad ? 0.0f : p[i] * s.up;
-  }
-}
-
 template <int VEC>
 __device__ __forceinline__ void store_codes(int8_t* q, const float p[VEC], const RowScale& s, bool exact, int n) {
   uint32_t c[VEC];
   codes<VEC>(p, s, exact, c);
   if constexpr (VEC == 8) {
     if (n >= VEC) {
-      uint2 w;
-      w.x = prmt(prmt(c[0], c[1], 0x0040), prmt(c[2], c[3], 0x0040), 0x5410);
-      w.y = prmt(prmt(c[4], c[5], 0x0040), prmt(c[6], c[7], 0x0040), 0x5410);
-      *reinterpret_cast<uint2*>(q) = w;
+      *reinterpret_cast<uint2*>(q) = pack_codes(c);
       return;
     }
   }
@@ -304,15 +199,6 @@ __device__ __forceinline__ void copy_vector(uint4* to, const __nv_bfloat16* from
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
                "l"(from), "r"(2 * min(n, 8))
                : "memory");
-}
-
-__device__ __forceinline__ void unpack(uint4 a, float v[8]) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
 }
 
 template <int VEC>
@@ -372,11 +258,6 @@ __device__ __forceinline__ void put_row(const RowArgs& a, long long row, int i, 
   }
 }
 
-__device__ __forceinline__ float warp_max(float m) {
-  // magnitudes compare as their bits do, a NaN above infinity
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu));
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -413,6 +294,7 @@ __device__ __forceinline__ void reduce(float& m, float& sum, int buf) {
 template <bool RES, bool NORM, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ? 8 : 1024 / THREADS)
     row_kernel(const __grid_constant__ RowArgs a) {
+  begin(a);
   typedef __nv_bfloat16 bf;
   constexpr bool kWarp = THREADS == 32;
   constexpr int kCta = kWarp ? 128 : THREADS;
@@ -470,6 +352,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ?
 // where one row's latency counts, and rows of fp32.
 template <typename XT, typename RT, bool NORM, int NV>
 __global__ void __launch_bounds__(1024) direct_row_kernel(const __grid_constant__ RowArgs a) {
+  begin(a);
   const long long row = blockIdx.x;
   float p[NV][8];
   float sum = 0.0f, m = 0.0f;
@@ -525,6 +408,7 @@ __global__ void __launch_bounds__(1024) odd_row_kernel(const __grid_constant__ R
 // first, so out may be x and res_out may be res or x.
 template <typename XT, typename RT, bool NORM>
 __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ RowArgs a) {
+  begin(a);
   const long long row = blockIdx.x;
   float sum = 0.0f, m = 0.0f;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
@@ -566,8 +450,7 @@ cudaError_t launch_rows(const RowArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return cudaErrorInvalidValue;
-  kernel<<<(unsigned)grid, cta, smem, s>>>(a);
-  return cudaGetLastError();
+  return start(kernel, a, grid, cta, smem, s);
 }
 
 bool aligned(const void* p, long long ld, int esize, int vec_bytes) {
@@ -601,8 +484,9 @@ int launch(const RowArgs& a, bool vec, cudaStream_t s) {
       return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
     }
   }
+  cudaError_t e;
   if (units > 4096) {
-    row_loop_kernel<XT, RT, NORM><<<a.T, 1024, 0, s>>>(a);
+    e = start(row_loop_kernel<XT, RT, NORM>, a, a.T, 1024, 0, s);
   } else {
     // fp32 (twice the bytes a vector, so enough are under way): 8192 rows of
     // 6144 with an fp32 residual 113 us (6.7 TB/s) with two vectors a thread,
@@ -610,19 +494,19 @@ int launch(const RowArgs& a, bool vec, cudaStream_t s) {
     const int nv = units > 2048 || (!vec && many && units > 512) ? 4 : (units > 1024 || (many && units > 256) ? 2 : 1);
     const int threads = ((units + nv - 1) / nv + 31) / 32 * 32;
     if (vec && nv == 1)
-      direct_row_kernel<XT, RT, NORM, 1><<<a.T, threads, 0, s>>>(a);
+      e = start(direct_row_kernel<XT, RT, NORM, 1>, a, a.T, threads, 0, s);
     else if (vec && nv == 2)
-      direct_row_kernel<XT, RT, NORM, 2><<<a.T, threads, 0, s>>>(a);
+      e = start(direct_row_kernel<XT, RT, NORM, 2>, a, a.T, threads, 0, s);
     else if (vec)
-      direct_row_kernel<XT, RT, NORM, 4><<<a.T, threads, 0, s>>>(a);
+      e = start(direct_row_kernel<XT, RT, NORM, 4>, a, a.T, threads, 0, s);
     else if (nv == 1)
-      odd_row_kernel<XT, RT, NORM, 1><<<a.T, threads, 0, s>>>(a);
+      e = start(odd_row_kernel<XT, RT, NORM, 1>, a, a.T, threads, 0, s);
     else if (nv == 2)
-      odd_row_kernel<XT, RT, NORM, 2><<<a.T, threads, 0, s>>>(a);
+      e = start(odd_row_kernel<XT, RT, NORM, 2>, a, a.T, threads, 0, s);
     else
-      odd_row_kernel<XT, RT, NORM, 4><<<a.T, threads, 0, s>>>(a);
+      e = start(odd_row_kernel<XT, RT, NORM, 4>, a, a.T, threads, 0, s);
   }
-  return cudaGetLastError() == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
+  return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
 bool row_type(int t) { return t == MOE_Q4_BF16 || t == MOE_Q4_F32; }
@@ -648,6 +532,15 @@ extern "C" int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T
   const cudaStream_t s = (cudaStream_t)stream;
   return x_type == MOE_Q4_F32 ? launch<float, NoRes, false>(a, vec, s)
                               : launch<__nv_bfloat16, NoRes, false>(a, vec, s);
+}
+
+int q4_launch_quant_chained(const void* x, long long ldx, int T, int K, int8_t* q, long long ldq, float* scale,
+                            cudaStream_t s) {
+  RowArgs a = {};
+  a.x = x, a.ldx = ldx;
+  a.q = q, a.ldq = ldq, a.scale = scale;
+  a.T = T, a.H = K, a.exact = 1, a.chained = 1;
+  return launch<__nv_bfloat16, NoRes, false>(a, aligned(x, ldx, 2, 16) && aligned(q, ldq, 1, 8), s);
 }
 
 extern "C" int moe_q4_add_norm(const void* x, int x_type, long long ldx, const void* residual, int residual_type,

@@ -437,7 +437,8 @@ MOE_Q4_API int moe_q4_combine(const float* y, const float* w, const int32_t* inv
  * Matrices of these calls have a row stride in elements (ld...), at least the
  * row's length, and consecutive elements in a row; int8 operands of products
  * start on 16 bytes and have row strides that are multiples of 16 (bytes past
- * a row's end are neither read nor written).  Element types of the others:
+ * a row's end are never written and do not matter; none past the last row's
+ * end is read).  Element types of the others:
  * ------------------------------------------------------------------------- */
 #define MOE_Q4_BF16 0
 #define MOE_Q4_F32 1
