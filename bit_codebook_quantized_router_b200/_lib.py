@@ -492,22 +492,28 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _device(t):
+def _first(t, what, dtypes):
+    """A call's first matrix: its device, shape and row stride."""
     dev = t.get_device()
-    if dev < 0 or t.dim() != 2:
-        raise ValueError("the operands must be CUDA matrices")
-    return dev
+    if dev < 0 or t.dtype not in dtypes or t.dim() != 2:
+        raise ValueError(f"{what} must be a CUDA matrix of {' or '.join(str(d) for d in dtypes)}")
+    n, k = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and k > 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+    return dev, n, k, ld if n > 1 else -(-k // 16) * 16
 
 
 def _rows(t, what, dev, n, k, dtypes):
     """Check a [n, k] matrix of consecutive elements in each row; its row stride
     in elements (that of a single row is of no consequence)."""
-    shape, (ld, inner) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
-    if shape != (n, k) or t.dtype not in dtypes or t.get_device() != dev or (inner != 1 and k > 1):
-        raise ValueError(f"{what} must be a matrix [{n}, {k}] of {' or '.join(str(d) for d in dtypes)} with "
-                         f"consecutive elements in a row, on cuda:{dev}; not {t.dtype} {list(shape)} with strides "
-                         f"{t.stride()} on {t.device}")
-    return ld if n > 1 else -(-k // 16) * 16
+    if t.shape == (n, k) and t.dtype in dtypes and t.get_device() == dev:
+        ld, inner = t.stride()
+        if inner == 1 or k <= 1:
+            return ld if n > 1 else -(-k // 16) * 16
+    raise ValueError(f"{what} must be a matrix [{n}, {k}] of {' or '.join(str(d) for d in dtypes)} with consecutive "
+                     f"elements in a row, on cuda:{dev}; not {t.dtype} {list(t.shape)} with strides {t.stride()} on "
+                     f"{t.device}")
 
 
 def _vector(t, what, dev, n, dtypes=_FP32):
@@ -546,9 +552,7 @@ def quant_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tens
     """bf16 or fp32 rows x [T, K] -> (codes int8 [T, K], scales fp32 [T]): for
     each row scale = max|x| / 127 and the codes nearest to 127 x / max|x|, ties
     to even.  A new q has rows on 16-byte boundaries (linear_i8's operands)."""
-    dev = _device(x)
-    T, K = x.shape
-    ldx = _rows(x, "x", dev, T, K, _ROW_TYPE)
+    dev, T, K, ldx = _first(x, "x", _ROW_TYPE)
     made = []
     if q is None:
         q = _codes(T, K, x.device)
@@ -572,9 +576,7 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
     residual, out bf16 [T, H] or None with bf16=False, codes int8 [T, H] and
     scales fp32 [T] or None with quant=False).  residual_out may be residual
     itself (in place), out may be a bf16 x."""
-    dev = _device(x)
-    T, H = x.shape
-    ldx = _rows(x, "x", dev, T, H, _ROW_TYPE)
+    dev, T, H, ldx = _first(x, "x", _ROW_TYPE)
     made = []
     ldr = ldro = ldo = ldq = rt = wt = 0
     rp = rop = wp = op = qp = sp = None
@@ -615,16 +617,14 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     (dtype, or out's), plus an fp32 bias [N].  The rows of x and w start on
     16-byte boundaries (quant_rows makes them so).  status: an int32 CUDA
     tensor [1] that receives the code of a device wait that gave up."""
-    dev = _device(x)
-    T, K = x.shape
+    dev, T, K, ldx = _first(x, "x", _INT8)
     N = w.shape[0]
     made = []
     if out is None:
         out = torch.empty((T, N), dtype=dtype, device=x.device)
         made.append(out)
-    _call("moe_q4_linear_i8", dev, stream, made, lib().moe_q4_linear_i8, x.data_ptr(),
-          _rows(x, "x", dev, T, K, _INT8), _vector(x_scale, "x_scale", dev, T), w.data_ptr(),
-          _rows(w, "w", dev, N, K, _INT8), _vector(w_scale, "w_scale", dev, N),
+    _call("moe_q4_linear_i8", dev, stream, made, lib().moe_q4_linear_i8, x.data_ptr(), ldx,
+          _vector(x_scale, "x_scale", dev, T), w.data_ptr(), _rows(w, "w", dev, N, K, _INT8), _vector(w_scale, "w_scale", dev, N),
           None if bias is None else _vector(bias, "bias", dev, N), T, N, K, out.data_ptr(),
           _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, N, _ROW_TYPE),
           None if status is None else _vector(status, "status", dev, 1, _INT32))
@@ -639,12 +639,10 @@ class MlpI8:
 
     def __init__(self, gate_up: torch.Tensor, gate_up_scale: torch.Tensor, down: torch.Tensor,
                  down_scale: torch.Tensor):
-        dev = _device(gate_up)
-        n, self.H = gate_up.shape
+        dev, n, self.H, ldg = _first(gate_up, "gate_up", _INT8)
         if n % 2:
             raise ValueError("gate_up holds the gate's rows and as many rows of the up projection")
         self.I = n // 2
-        ldg = _rows(gate_up, "gate_up", dev, n, self.H, _INT8)
         ldd = _rows(down, "down", dev, self.H, self.I, _INT8)
         gp, dp = _vector(gate_up_scale, "gate_up_scale", dev, n), _vector(down_scale, "down_scale", dev, self.H)
         self.tensors = gate_up, gate_up_scale, down, down_scale
@@ -661,8 +659,9 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
            stream=None) -> torch.Tensor:
     """The int8 SwiGLU MLP: int8 rows x [T, H] with scales x_scale [T] -> out
     [T, H] in bf16 or fp32 (dtype, or out's); status as for linear_i8."""
-    dev = _device(x)
-    T, H = x.shape[0], mlp.H
+    dev, T, H, ldx = _first(x, "x", _INT8)
+    if H != mlp.H:
+        raise ValueError(f"x must have the MLP's {mlp.H} columns, not {H}")
     made = []
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=x.device)
@@ -674,8 +673,8 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
         raise ValueError(f"ws must be uint8 on cuda:{dev} (alloc_workspace)")
     if mlp.tensors[0].get_device() != dev:
         raise ValueError(f"the MLP's weights must be on cuda:{dev}")
-    _call("moe_q4_mlp_i8", dev, stream, made, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(),
-          _rows(x, "x", dev, T, H, _INT8), _vector(x_scale, "x_scale", dev, T), T, out.data_ptr(),
+    _call("moe_q4_mlp_i8", dev, stream, made, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(), ldx,
+          _vector(x_scale, "x_scale", dev, T), T, out.data_ptr(),
           _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, H, _ROW_TYPE),
           None if status is None else _vector(status, "status", dev, 1, _INT32), ws.data_ptr(), ws.numel())
     return out
@@ -689,6 +688,6 @@ def _shared_rows(layer, shared, xq, x_scale, T):
         return 0
     if not isinstance(shared, MlpI8):
         raise ValueError("xq and x_scale are read by an int8 shared expert (MlpI8)")
-    dev = _device(xq)
+    dev = xq.get_device()
     _vector(x_scale, "x_scale", dev, T)
     return _rows(xq, "xq", dev, T, layer.H, _INT8)

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 3 : 1) few_kernel(const __grid_
     const float xs = HALF ? s_xs[t] : a.xs[t];
     float y = scaled(v, xs, a.ws[n]);
     if (GATED)
-      y = silu_mul(y, scaled(u, xs, a.ws[a.N + n]));
+      y = silu_mul_fast(y, scaled(u, xs, a.ws[a.N + n]));
     else if (a.bias)
       y += a.bias[n];
     store_out(a, t, n, y);

@@ -22,6 +22,7 @@
 #include <cuda.h>
 
 #include "linear8.cuh"
+#include "rows8.cuh"
 #include "sm100.cuh"
 
 namespace q4 {
@@ -101,11 +102,16 @@ __global__ void __launch_bounds__(kThreads)
     mbar_init(acc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // the ring's first loads, before anything is set up beside them; the
-    // weights' before the kernel in front is done with the tokens
-    for (int i = 0; i < S && k_lo + i < k_hi; ++i) load_w(k_lo + i, i);
-    pdl_wait();
-    for (int i = 0; i < S && k_lo + i < k_hi; ++i) load_x(k_lo + i, i);
+    // the ring's first loads, before anything is set up beside them; in a
+    // chain the weights' before the kernel in front is done with the tokens
+    for (int i = 0; i < S && k_lo + i < k_hi; ++i) {
+      load_w(k_lo + i, i);
+      if (!a.chained) load_x(k_lo + i, i);
+    }
+    if (a.chained) {
+      pdl_wait();
+      for (int i = 0; i < S && k_lo + i < k_hi; ++i) load_x(k_lo + i, i);
+    }
   }
   __syncwarp();
   pdl_wait();
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(kThreads)
       const float xs = s_xs[c];
       float y = scaled(v, xs, wscale);
       if (GATED)
-        y = silu_mul(y, scaled(u, xs, uscale));
+        y = silu_mul_fast(y, scaled(u, xs, uscale));
       else if (a.bias)
         y += bias;
       store_out(a, c_lo + c, n, y);
@@ -346,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
-      bool ok = true, filled = false;
+      bool ok = true, filled = !a.chained;
       for (int tile = first; tile < total && ok; tile += step) {
         const int m = tile % m_tiles, n = tile / m_tiles;
         const int ya = m * 256 + rank * 128;
@@ -357,8 +363,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kTile + BN / 2 * kBK));
           const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
           tma_load_2d_pair(sB + s * kTile, &tm_w, bar, ks * kBK, yb);
-          // the ring's first weights are asked for before the kernel in front
-          // is done with the tokens
+          // in a chain the ring's first weights are asked for before the
+          // kernel in front is done with the tokens (elsewhere step by step:
+          // weights first costs 1 us)
           if (!filled) {
             if ((int)it + 1 < min(kWideStages, ksteps)) continue;
             pdl_wait();
@@ -441,14 +448,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int c = half * kCols + i * 16;
         const float* sc = s_scale + buf * 256 + c;
         const float* sb = s_bias + buf * 256 + c;
+        const F2 xs2 = f2(xs, xs);
         float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          y[j] = scaled((int)v[i & 1][j], xs, sc[j]);
-          if (GATED)
-            y[j] = silu_mul(y[j], scaled((int)u[i & 1][j], xs, sc[kBN + j]));
-          else if (a.bias)
-            y[j] += sb[j];
+        for (int j = 0; j < 16; j += 4) {
+          // (as scaled(), two at a time)
+          const float4 w = *reinterpret_cast<const float4*>(sc + j);
+          const uint32_t* q = v[i & 1] + j;
+          split(mul(f2((float)(int)q[0], (float)(int)q[1]), mul(xs2, f2(w.x, w.y))), y[j], y[j + 1]);
+          split(mul(f2((float)(int)q[2], (float)(int)q[3]), mul(xs2, f2(w.z, w.w))), y[j + 2], y[j + 3]);
+          if (GATED) {
+            const float4 g = *reinterpret_cast<const float4*>(sc + kBN + j);
+            const uint32_t* p = u[i & 1] + j;
+            float z[4];
+            split(mul(f2((float)(int)p[0], (float)(int)p[1]), mul(xs2, f2(g.x, g.y))), z[0], z[1]);
+            split(mul(f2((float)(int)p[2], (float)(int)p[3]), mul(xs2, f2(g.z, g.w))), z[2], z[3]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) y[j + h] = silu_mul_fast(y[j + h], z[h]);
+          } else if (a.bias) {
+            const float4 b = *reinterpret_cast<const float4*>(sb + j);
+            y[j] += b.x, y[j + 1] += b.y, y[j + 2] += b.z, y[j + 3] += b.w;
+          }
         }
         store_row16(a, align, stage, t, n0 + c, y);
         __syncwarp();
