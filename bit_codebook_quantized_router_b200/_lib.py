@@ -523,9 +523,8 @@ def _vector(t, what, dev, n, dtypes=_FP32):
     return t.data_ptr()
 
 
-def _call(what, dev, stream, made, fn, *args):
-    """fn(*args, stream handle) with the tensors' device as the current one.
-    `made`: what the binding allocated for the call (see _hold)."""
+def _call(what, dev, stream, fn, *args):
+    """fn(*args, stream handle) with the tensors' device as the current one."""
     if stream is None:
         handle = _raw_stream(dev)
     elif stream.device.index != dev:
@@ -539,13 +538,19 @@ def _call(what, dev, stream, made, fn, *args):
             rc = fn(*args, handle)
     if rc != OK:
         raise MoeQ4Error(rc, what)
-    if stream is not None:
-        _hold(stream, *made)
 
 
-def _codes(T, K, dev):
+def _new(shape, dtype, like, stream):
+    """A result's memory, allocated on the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _codes(T, K, like, stream):
     """An int8 [T, K] whose rows start on 16 bytes, as the products read them."""
-    return torch.empty((T, -(-K // 16) * 16), dtype=torch.int8, device=dev)[:, :K]
+    return _new((T, -(-K // 16) * 16), torch.int8, like, stream)[:, :K]
 
 
 def quant_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
@@ -553,14 +558,11 @@ def quant_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tens
     each row scale = max|x| / 127 and the codes nearest to 127 x / max|x|, ties
     to even.  A new q has rows on 16-byte boundaries (linear_i8's operands)."""
     dev, T, K, ldx = _first(x, "x", _ROW_TYPE)
-    made = []
     if q is None:
-        q = _codes(T, K, x.device)
-        made.append(q)
+        q = _codes(T, K, x, stream)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=x.device)
-        made.append(scale)
-    _call("moe_q4_quant_rows", dev, stream, made, lib().moe_q4_quant_rows, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, T, K,
+        scale = _new((T,), torch.float32, x, stream)
+    _call("moe_q4_quant_rows", dev, stream, lib().moe_q4_quant_rows, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, T, K,
           q.data_ptr(), _rows(q, "q", dev, T, K, _INT8), _vector(scale, "scale", dev, T))
     return q, scale
 
@@ -577,15 +579,13 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
     scales fp32 [T] or None with quant=False).  residual_out may be residual
     itself (in place), out may be a bf16 x."""
     dev, T, H, ldx = _first(x, "x", _ROW_TYPE)
-    made = []
     ldr = ldro = ldo = ldq = rt = wt = 0
     rp = rop = wp = op = qp = sp = None
     if residual is not None:
         dtype = residual.dtype
         ldr, rp = _rows(residual, "residual", dev, T, H, _ROW_TYPE), residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty((T, H), dtype=dtype, device=x.device)
-            made.append(residual_out)
+            residual_out = _new((T, H), dtype, x, stream)
         ldro, rop, rt = _rows(residual_out, "residual_out", dev, T, H, (dtype,)), residual_out.data_ptr(), _ROW_TYPE[dtype]
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
@@ -593,18 +593,15 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
         wp, wt = _vector(weight, "weight", dev, H, _ROW_TYPE), _ROW_TYPE[weight.dtype]
     if bf16 or out is not None:
         if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-            made.append(out)
+            out = _new((T, H), torch.bfloat16, x, stream)
         ldo, op = _rows(out, "out", dev, T, H, _BF16), out.data_ptr()
     if quant or q is not None or scale is not None:
         if q is None:
-            q = _codes(T, H, x.device)
-            made.append(q)
+            q = _codes(T, H, x, stream)
         if scale is None:
-            scale = torch.empty(T, dtype=torch.float32, device=x.device)
-            made.append(scale)
+            scale = _new((T,), torch.float32, x, stream)
         ldq, qp, sp = _rows(q, "q", dev, T, H, _INT8), q.data_ptr(), _vector(scale, "scale", dev, T)
-    _call("moe_q4_add_norm", dev, stream, made, lib().moe_q4_add_norm, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, rp, rt,
+    _call("moe_q4_add_norm", dev, stream, lib().moe_q4_add_norm, x.data_ptr(), _ROW_TYPE[x.dtype], ldx, rp, rt,
           ldr, rop, ldro, wp, wt, eps, T, H, op, ldo, qp, ldq, sp)
     return residual_out, out, q, scale
 
@@ -619,11 +616,9 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     tensor [1] that receives the code of a device wait that gave up."""
     dev, T, K, ldx = _first(x, "x", _INT8)
     N = w.shape[0]
-    made = []
     if out is None:
-        out = torch.empty((T, N), dtype=dtype, device=x.device)
-        made.append(out)
-    _call("moe_q4_linear_i8", dev, stream, made, lib().moe_q4_linear_i8, x.data_ptr(), ldx,
+        out = _new((T, N), dtype, x, stream)
+    _call("moe_q4_linear_i8", dev, stream, lib().moe_q4_linear_i8, x.data_ptr(), ldx,
           _vector(x_scale, "x_scale", dev, T), w.data_ptr(), _rows(w, "w", dev, N, K, _INT8), _vector(w_scale, "w_scale", dev, N),
           None if bias is None else _vector(bias, "bias", dev, N), T, N, K, out.data_ptr(),
           _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, N, _ROW_TYPE),
@@ -662,18 +657,15 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
     dev, T, H, ldx = _first(x, "x", _INT8)
     if H != mlp.H:
         raise ValueError(f"x must have the MLP's {mlp.H} columns, not {H}")
-    made = []
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=x.device)
-        made.append(out)
+        out = _new((T, H), dtype, x, stream)
     if ws is None:
-        ws = alloc_workspace(mlp_i8_workspace(mlp, T), x.device)
-        made.append(ws)
+        ws = _new((max(mlp_i8_workspace(mlp, T), 256),), torch.uint8, x, stream)
     elif ws.get_device() != dev or ws.dtype != torch.uint8:
         raise ValueError(f"ws must be uint8 on cuda:{dev} (alloc_workspace)")
     if mlp.tensors[0].get_device() != dev:
         raise ValueError(f"the MLP's weights must be on cuda:{dev}")
-    _call("moe_q4_mlp_i8", dev, stream, made, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(), ldx,
+    _call("moe_q4_mlp_i8", dev, stream, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(), ldx,
           _vector(x_scale, "x_scale", dev, T), T, out.data_ptr(),
           _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, H, _ROW_TYPE),
           None if status is None else _vector(status, "status", dev, 1, _INT32), ws.data_ptr(), ws.numel())

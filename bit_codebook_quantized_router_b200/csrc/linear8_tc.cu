@@ -3,16 +3,27 @@
 //
 // mid_kernel, up to 64 tokens: the weights' bytes bound it.  The MMA's M is 128
 // weight rows and its N all the tokens, so each weight is read once; K is split
-// over the CTAs of a cluster so that every SM streams weights.  The partial
-// sums are int32, so adding them is exact in any order: each CTA sends the
-// columns that another owns to that CTA's shared memory, and each finishes its
-// own columns.  No workspace and one launch.
+// over the CTAs of a cluster, two CTAs an SM, so that every SM streams weights.
+// The partial sums are int32, so adding them is exact in any order: each CTA
+// sends the columns that another owns to that CTA's shared memory, and each
+// finishes its own columns.  No workspace and one launch.  Measured, N = K =
+// 6144 from memory: 17 tokens 11.5 us, 64 tokens 13.3 (2.9 TB/s with the
+// launch): weights arrive from 2.4 to 8.7 us of it at 6.3 TB/s, the exchange and
+// the last step take 4.  With the weights as the MMA's N = 256 and the tokens as
+// its M, 64 tokens took 22 us: twice the sums to exchange, by half the warps.
 //
 // wide_kernel, more tokens: pairs of CTAs (cta_group::2) multiply 256 tokens
 // by 256 weight rows, each CTA holding 128 rows of both operands, so a pair
 // reads half of what two CTAs with tiles of 128 x 256 would; persistent, with
 // two accumulators, so that one tile's results leave while the next is
-// multiplied.
+// multiplied.  An MMA of 256 x 256 x 32 takes 129 cycles (128 is the units'
+// rate); one of a single CTA, 128 rows, takes 170 whatever its N.  Measured:
+// 8192 tokens, N = K = 6144 200 us, 3.09 POP/s (1.88 times the measured bf16
+// rate; the tensor pipe is busy 85% of the time that SMs are, at 1.66 GHz under
+// the power limit); 2048 tokens 54 us; 256 tokens, K = 2048 11.2 us.  A tile's
+// results take 4 us to leave, hidden but for the last tile's; staging them in
+// shared memory for whole lines or for TMA stores was no faster end to end
+// (2048 tokens, K = 2048: 23.6 us as it is, 25.2 to 26.0 so).
 //
 // Both read operands by TMA into the 128-byte-swizzle K-major layout, in
 // k-steps of 128 bytes; what lies past a row, a matrix or K arrives as zeros.
@@ -56,13 +67,14 @@ __device__ __forceinline__ void give_up(int32_t* status, uint64_t* full, int sta
     }
 }
 
-// ---- up to 256 tokens -----------------------------------------------------------
+// ---- up to 64 tokens ------------------------------------------------------------
 
 struct MidPlan {
   int bn;       // tokens, rounded up to 16
   int own;      // columns that a CTA of the cluster finishes (a multiple of 8)
   int stages;   // ring stages
   int ksteps;   // k-steps of 128 in K
+  int inbox;    // byte offset of the other CTAs' partial sums, behind the ring
 };
 
 template <bool GATED>
@@ -70,7 +82,7 @@ __global__ void __launch_bounds__(kThreads)
     mid_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ MidPlan p,
                const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ uint64_t full[kMidStages], empty[kMidStages], acc_full[1];
+  __shared__ uint64_t full[kMidStages], empty[kMidStages], acc_full[1], in_full[1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ float s_xs[kLinearMidTokens];
@@ -100,6 +112,7 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(in_full, splits * kEpiWarps);
     *abort_flag = 0;
     fence_mbar_init();
     // the ring's first loads, before anything is set up beside them; in a
@@ -114,8 +127,6 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncwarp();
-  pdl_wait();
-  pdl_trigger();
   if (warp == 1) {
     tmem_alloc(&tmem_slot, cols);
     tmem_relinquish();
@@ -126,16 +137,16 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kRows = GATED ? 64 : 128;
   const int n = n0 + (et & (kRows - 1));
   float wscale = 0.0f, uscale = 0.0f, bias = 0.0f;
-  if (et >= 0) {
-    if (n < a.N) {
-      wscale = a.ws[n];
-      if (GATED) uscale = a.ws[a.N + n];
-      if (!GATED && a.bias) bias = a.bias[n];
-    }
-    if (et < c_n) s_xs[et] = a.xs[c_lo + et];
+  pdl_wait();  // (before these loads: it waits for them)
+  pdl_trigger();
+  if (et >= 0 && n < a.N) {
+    wscale = a.ws[n];
+    if (GATED) uscale = a.ws[a.N + n];
+    if (!GATED && a.bias) bias = a.bias[n];
   }
   tc_fence_before();
   __syncthreads();
+  cluster_arrive_relaxed();  // this CTA's barriers are ready (waited for before anything is sent)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
@@ -167,25 +178,24 @@ __global__ void __launch_bounds__(kThreads)
       umma_commit(acc_full);
       mbar_wait(acc_full, 0, abort_flag, kWaitNs);
     }
+  } else if (et < c_n) {
+    s_xs[et] = a.xs[c_lo + et];
   }
   __syncthreads();
-  // every copy has been read by an MMA and every MMA is done, or a wait was
-  // given up: the ring's memory is free here
+  // every MMA is done, or a wait was given up
   if (threadIdx.x == 0 && *abort_flag) give_up(a.status, full, S);
   __syncwarp();
-  if (splits > 1) {
-    cluster_arrive();  // and past the barrier in every CTA of the cluster
-    cluster_wait();
-  }
-  // send: columns [own * r, own * (r + 1)) to CTA r as [src][column][128 rows],
-  // a warp 128 consecutive bytes at a time (16 bytes a lane at a row's pitch
-  // measured slower, 17.1 against 14.6 us at 64 tokens and 6144 x 6144, and so
-  // did bulk copies of what was gathered here first, 15.6)
+  cluster_wait();
   tc_fence_after();
   if (warp >= kEpiWarp0) {
+    // send: columns [own * r, own * (r + 1)) to CTA r as [src][column][128
+    // rows], a warp 128 consecutive bytes at a time (16 bytes a lane at a row's
+    // pitch measured slower, 17.1 against 14.6 us at 64 tokens and 6144 x 6144,
+    // and so did bulk copies of what was gathered here first, 15.6)
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, row = quad * 32 + lane;
     const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t inbox = smem_u32(smem) + (rank * p.own * 128 + row) * 4;
+    const uint32_t inbox = smem_u32(smem) + p.inbox;
+    const uint32_t mine = inbox + (rank * p.own * 128 + row) * 4;
     for (int c0 = half * 16; c0 < p.bn; c0 += 32) {
       uint32_t v[16];
       tmem_ld16_nowait(tb + c0, v);
@@ -193,39 +203,47 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int h = 0; h < 16; h += 8) {
         const int to = (c0 + h) / p.own;
-        const uint32_t at = cluster_addr(inbox + (c0 + h - to * p.own) * 512, to);
+        const uint32_t at = cluster_addr(mine + (c0 + h - to * p.own) * 512, to);
 #pragma unroll
         for (int j = 0; j < 8; ++j) cluster_st32(at + j * 512, v[h + j]);
       }
     }
-  }
-  tc_fence_before();
-  if (splits > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
+    __syncwarp();
+    if (lane < splits) mbar_arrive_cluster(cluster_addr(smem_u32(in_full), lane));
+    __syncwarp();
+    tc_fence_before();
 
-  // finish this CTA's columns
-  if (et >= 0 && n < a.N) {
-    const int* box = reinterpret_cast<const int*>(smem) + (et & (kRows - 1));
-#pragma unroll 4
-    for (int c = et / kRows; c < c_n; c += 32 * kEpiWarps / kRows) {
-      int v = 0, u = 0;
-      for (int src = 0; src < splits; ++src) {
-        v += box[(src * p.own + c) * 128];
-        if (GATED) u += box[(src * p.own + c) * 128 + 64];
+    // finish this CTA's columns, four at a time, once all their sums are here
+    mbar_wait_warp<true>(in_full, 0, abort_flag, kWaitNs);
+    if (n < a.N) {
+      constexpr int kStep = 32 * kEpiWarps / kRows;
+      const uint32_t box = inbox + (et & (kRows - 1)) * 4;
+      for (int c0 = et / kRows; c0 < c_n; c0 += 4 * kStep) {
+        int v[4] = {}, u[4] = {};
+        for (int src = 0; src < splits; ++src)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = box + (src * p.own + min(c0 + j * kStep, c_n - 1)) * 512;
+            v[j] += (int)lds32(at);
+            if (GATED) u[j] += (int)lds32(at + 256);
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + j * kStep;
+          if (c >= c_n) break;
+          const float xs = s_xs[c];
+          float y = scaled(v[j], xs, wscale);
+          if (GATED)
+            y = silu_mul_fast(y, scaled(u[j], xs, uscale));
+          else if (a.bias)
+            y += bias;
+          store_out(a, c_lo + c, n, y);
+        }
       }
-      const float xs = s_xs[c];
-      float y = scaled(v, xs, wscale);
-      if (GATED)
-        y = silu_mul_fast(y, scaled(u, xs, uscale));
-      else if (a.bias)
-        y += bias;
-      store_out(a, c_lo + c, n, y);
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) record_error(a.status, MOE_Q4_ETIMEOUT);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -403,6 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (ok) umma_commit_pair(&acc_full[buf]);
       }
+      // the last tiles' arrivals from the pair's other CTA, so that none comes
+      // after this one's end
+      for (uint32_t u = use > 2 ? use - 2 : 0; u < use && ok; ++u)
+        ok = mbar_wait(&acc_empty[u & 1], (u >> 1) & 1, abort_flag, kWaitNs);
     }
   } else {
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, e = threadIdx.x - 32 * kEpiWarp0;
@@ -410,6 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     float* stage = s_rows + (warp - kEpiWarp0) * 32 * kWideRow;
     uint32_t use = 0;
+    bool lost = false;
     for (int tile = first; tile < total; tile += step, ++use) {
       const int m = tile % m_tiles, n0 = tile / m_tiles * kBN;
       const int buf = use & 1;
@@ -424,7 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const long long t = (long long)m * 256 + rank * 128 + quad * 32 + lane;
       const float xs = t < a.T ? a.xs[t] : 0.0f;
       named_bar(1, 32 * kEpiWarps);
-      if (!mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs)) break;
+      // (a warp whose wait was given up still meets the others at the barrier)
+      if (lost || (lost = !mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs))) continue;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
       constexpr int kCols = kBN / 2;  // of this warp
@@ -479,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) give_up(a.status, full, kWideStages);
   __syncthreads();
-  cluster_arrive();
+  cluster_arrive_relaxed();  // (a release would wait for the results' stores)
   cluster_wait();
   if (warp == 1) {
     __syncwarp();
@@ -538,9 +562,9 @@ int launch_mid(const LinArgs& a, cudaStream_t s) {
   while (splits < 8 && tiles * splits * 2 <= 2 * sms * 7 / 8 && p.ksteps >= 4 * splits) splits *= 2;
   p.own = (p.bn / 8 + splits - 1) / splits * 8;
   const int stage = kTile + p.bn * kBK, most = (p.ksteps + splits - 1) / splits, box = splits * p.own * 512;
-  p.stages = min(min(most, kMidStages), 108 * 1024 / stage);
-  if (p.stages * stage < box) p.stages = (box + stage - 1) / stage;  // (the ring takes the partial sums)
-  const int smem = p.stages * stage + 1024;
+  p.stages = min(min(most, kMidStages), (108 * 1024 - box) / stage);
+  p.inbox = p.stages * stage;
+  const int smem = p.inbox + box + 1024;
   CUtensorMap tx, tw;
   if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, p.bn) ||
       !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, GATED ? 64 : 128))

@@ -509,6 +509,8 @@ int launch(const RowArgs& a, bool vec, cudaStream_t s) {
   return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
+constexpr int kMaxRow = 1 << 30;  // values of a row (positions in 32 bits)
+
 bool row_type(int t) { return t == MOE_Q4_BF16 || t == MOE_Q4_F32; }
 
 bool elem_aligned(const void* p, int type) { return ((uintptr_t)p & (esize(type) - 1)) == 0; }
@@ -522,6 +524,7 @@ using namespace q4;
 extern "C" int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T, int K, int8_t* q, long long ldq,
                                  float* scale, void* stream) {
   if (!row_type(x_type) || T < 0 || K < 1 || ldx < K || ldq < K) return MOE_Q4_EINVAL;
+  if (K > kMaxRow) return MOE_Q4_ENOTSUP;
   if (T == 0) return MOE_Q4_OK;
   if (!x || !q || !scale || !elem_aligned(x, x_type) || ((uintptr_t)scale & 3)) return MOE_Q4_EINVAL;
   RowArgs a = {};
@@ -553,8 +556,13 @@ extern "C" int moe_q4_add_norm(const void* x, int x_type, long long ldx, const v
   if ((out && ldo < H) || (q && ldq < H)) return MOE_Q4_EINVAL;
   if ((residual == nullptr) != (residual_out == nullptr) || (q == nullptr) != (scale == nullptr))
     return MOE_Q4_EINVAL;
+  if (H > kMaxRow) return MOE_Q4_ENOTSUP;
   if (T == 0) return MOE_Q4_OK;
   if (!x || (!out && !q) || (out && out == residual_out)) return MOE_Q4_EINVAL;
+  // in place: a row's results have to go where that row, and no other, was read
+  if (residual && residual_out == residual && T > 1 && ldro != ldr) return MOE_Q4_EINVAL;
+  if (residual && residual_out == x && (residual_type != x_type || (T > 1 && ldro != ldx))) return MOE_Q4_EINVAL;
+  if (out && out == x && (x_type != MOE_Q4_BF16 || (T > 1 && ldo != ldx))) return MOE_Q4_EINVAL;
   if (!elem_aligned(x, x_type) || (residual && (!elem_aligned(residual, residual_type) ||
                                                 !elem_aligned(residual_out, residual_type))) ||
       (weight && !elem_aligned(weight, weight_type)) || ((uintptr_t)out & 1) || ((uintptr_t)scale & 3))

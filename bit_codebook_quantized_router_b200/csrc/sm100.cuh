@@ -72,14 +72,29 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 
+// The same, seeing what threads of other CTAs of the cluster wrote before they
+// arrived.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for phase `parity` of `bar` to complete, giving up after `limit_ns`
 // (or as soon as another role of the CTA has set *abort).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (CLUSTER ? mbar_try_wait_cluster(bar, parity, 0u) : mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity, 20000u) : mbar_try_wait_suspend(bar, parity, 20000u)) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       *abort = 1;
@@ -90,9 +105,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // mbar_wait by every lane of a warp, then a vote, so the whole warp goes on
 // or gives up together (no lane is left behind at a later warp barrier).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                uint64_t limit_ns) {
-  const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+  const bool got = __all_sync(0xffffffffu, mbar_wait<CLUSTER>(bar, parity, abort, limit_ns));
   if (!got) *abort = 1;
   return got;
 }
@@ -327,6 +343,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 // Every thread of the cluster's CTAs: what was written before is seen after.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// Without the wait for this thread's own accesses (2 us behind loads that
+// memory is busy with): for barriers made known by fence_mbar_init.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // The shared::cluster address of this CTA's `addr` in the CTA of rank `rank`.

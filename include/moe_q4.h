@@ -445,7 +445,7 @@ MOE_Q4_API int moe_q4_combine(const float* y, const float* w, const int32_t* inv
 
 /* moe_q4_quant_rows -- T rows to codes and scales.
  *   x      device, bf16 or fp32 (x_type) [T][ldx];
- *   T >= 0; K >= 1;
+ *   T >= 0; 1 <= K <= 2^30 (MOE_Q4_ENOTSUP above);
  *   q      device int8 [T][ldq] (out);  scale  device fp32 [T] (out).
  * The codes are exact as defined above; scale is one fp32 division.
  * Alignment of x and q is that of their elements; 16-byte (x) and 8-byte (q)
@@ -464,10 +464,10 @@ MOE_Q4_API int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T
  *   x             device, bf16 or fp32 (x_type) [T][ldx];
  *   residual      optional device, bf16 or fp32 (residual_type) [T][ldr], and
  *   residual_out  device, the same type, [T][ldro] (out): both or neither;
- *                 residual_out may be residual, or x where type and stride
- *                 are the same;
+ *                 residual_out may be residual (the same stride), or x (the
+ *                 same type and stride): MOE_Q4_EINVAL otherwise;
  *   weight        optional device, bf16 or fp32 (weight_type) [H], NULL: ones;
- *   eps           > 0, finite;  T >= 0; H >= 1;
+ *   eps           > 0, finite;  T >= 0; 1 <= H <= 2^30 (MOE_Q4_ENOTSUP above);
  *   out           optional device bf16 [T][ldo] (out); may be a bf16 x of the
  *                 same stride, not residual_out;
  *   q, scale      optional device int8 [T][ldq], fp32 [T] (out): both or

@@ -28,6 +28,7 @@ def test_quant_rows_refusals(L):
                 dict(ldx=63), dict(ldq=63), dict(x=P + 1), dict(x=P + 2, xt=F32), dict(scale=P + 2)):
         assert f(**bad) == _lib.EINVAL, bad
     assert f(T=0, x=None, q=None, scale=None) == _lib.OK
+    assert f(K=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31) == _lib.ENOTSUP
 
 
 def test_add_norm_refusals(L):
@@ -41,6 +42,11 @@ def test_add_norm_refusals(L):
                 dict(ro=Q + 2), dict(w=P + 1), dict(out=P + 1), dict(scale=P + 1)):
         assert f(**bad) == _lib.EINVAL, bad
     assert f(T=0, x=None) == _lib.OK
+    # in place only where a row's results go where that row was read
+    for bad in (dict(ro=P, res=P, ldr=64, ldro=72), dict(x=P, ro=P, res=Q, rt=F32), dict(xt=F32, ro=P, res=Q, ldro=72),
+                dict(x=P, out=P, xt=F32), dict(x=P, out=P, ldo=72)):
+        assert f(**bad) == _lib.EINVAL, bad
+    assert f(H=(1 << 30) + 1, **{k: 1 << 31 for k in ("ldx", "ldr", "ldro", "ldo", "ldq")}) == _lib.ENOTSUP
 
 
 def test_linear_refusals(L):
