@@ -87,34 +87,29 @@ __device__ __forceinline__ void few_codes(const LinArgs& a, int8_t* s_x, int pit
   }
 }
 
-// The 16 bytes of a row at k.  Past the row's end K: in the last row nothing
-// is read there and zeros stand for it; in another row, what lies between the
-// rows (in the 16 bytes that hold the row's end) is taken as it is.
-__device__ __forceinline__ uint4 load_row16(const int8_t* row, int k, int K, bool last) {
-  const int n = K - k;
-  if (n >= 16 || (n > 0 && !last)) return *reinterpret_cast<const uint4*>(row + k);
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (n > 0) {
-    const int8_t* p = row + k;
-    uint32_t lo = 0, tail = 0;
-    uint2 d = make_uint2(0, 0);
-    if (n & 8) d = *reinterpret_cast<const uint2*>(p);
-    if (n & 4) lo = *reinterpret_cast<const uint32_t*>(p + (n & 8));
-    if (n & 2) tail = *reinterpret_cast<const uint16_t*>(p + (n & 12));
-    if (n & 1) tail |= (uint32_t)(uint8_t)p[n & 14] << (8 * (n & 2));
-    const uint32_t e = n & 4 ? lo : tail, f = n & 4 ? tail : 0;
-    v = n & 8 ? make_uint4(d.x, d.y, e, f) : make_uint4(e, f, 0, 0);
-  }
-  return v;
+// The first n (1 to 15) bytes at p (16-byte aligned), and zeros.
+__device__ __noinline__ uint4 load_some(const int8_t* p, int n) {
+  uint32_t lo = 0, tail = 0;
+  uint2 d = make_uint2(0, 0);
+  if (n & 8) d = *reinterpret_cast<const uint2*>(p);
+  if (n & 4) lo = *reinterpret_cast<const uint32_t*>(p + (n & 8));
+  if (n & 2) tail = *reinterpret_cast<const uint16_t*>(p + (n & 12));
+  if (n & 1) tail |= (uint32_t)(uint8_t)p[n & 14] << (8 * (n & 2));
+  const uint32_t e = n & 4 ? lo : tail, f = n & 4 ? tail : 0;
+  return n & 8 ? make_uint4(d.x, d.y, e, f) : make_uint4(e, f, 0, 0);
 }
 
-// v with zeros from byte n on.
-__device__ __forceinline__ uint4 first_bytes(uint4 v, int n) {
-  auto part = [n](uint32_t w, int at) {
-    const int b = min(max(n - at, 0), 4);
-    return b == 4 ? w : w & ((1u << (8 * b)) - 1u);
-  };
-  return make_uint4(part(v.x, 0), part(v.y, 4), part(v.z, 8), part(v.w, 12));
+// The 16 bytes of a row at k, zeros past its end K (nothing is read there).
+__device__ __forceinline__ uint4 load_row16(const int8_t* row, int k, int K) {
+  if (k + 16 <= K) return *reinterpret_cast<const uint4*>(row + k);
+  return k < K ? load_some(row + k, K - k) : make_uint4(0, 0, 0, 0);
+}
+
+// The same of a weight row; what lies between the rows in the 16 bytes that
+// hold its end is taken as it is (it meets the tokens' zeros), but nothing is
+// read behind the last row.
+__device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, bool last) {
+  return k < K && !last ? ldg_stream(row + k) : load_row16(row, k, K);
 }
 
 // Few tokens: 16 weight rows a CTA (8 gate and 8 up rows when GATED), 8 NT
@@ -130,7 +125,7 @@ __device__ __forceinline__ uint4 first_bytes(uint4 v, int n) {
 // 8 tokens 8.9, 16 tokens 12.9; the memory's bandwidth and the launch bound it.
 // Three CTAs an SM (85 registers): with two, 384 CTAs take two turns (9.2 us).
 template <int NT, int U, bool GATED, bool HALF>
-__global__ void __launch_bounds__(256, NT == 1 ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {
+__global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ int s_acc[];  // [warps][8 NT][16]; HALF: and codes [8 NT][pitch] behind
   __shared__ float s_xs[8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -151,8 +146,7 @@ __global__ void __launch_bounds__(256, NT == 1 ? 3 : 1) few_kernel(const __grid_
     if (HALF) return *reinterpret_cast<const uint4*>(s_x + t * pitch + k);
     // (no read-only path: in a chain the rows are written while this kernel runs)
     if (whole) return *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
-    // (the weights' bytes past K meet these zeros)
-    return first_bytes(load_row16(a.x + t * a.ldx, k, a.K, t == a.T - 1), a.K - k);
+    return load_row16(a.x + t * a.ldx, k, a.K);
   };
   auto product = [&](int n, uint4 p, uint4 q, uint4 x) {
     mma_s8(acc[n], p.x, q.x, p.y, q.y, x.x, x.y);
@@ -205,9 +199,11 @@ __global__ void __launch_bounds__(256, NT == 1 ? 3 : 1) few_kernel(const __grid_
 #pragma unroll
       for (int n = 0; n < NT; ++n) product(n, p, q, load_x(n, k, true));
     }
-  for (int k = full * 128 + warp * 64 + 16 * t4; k < a.K + 16 * t4; k += warps * 64) {
-    const uint4 p = load_row16(wa, k, a.K, !GATED && ra == a.N - 1);
-    const uint4 q = load_row16(wb, k, a.K, rb == (GATED ? 2 * a.N : a.N) - 1);
+  // the rest, in halves of a segment, from the warps on that had fewest
+  const int rest = (warp + warps - full % warps) % warps;
+  for (int k = full * 128 + rest * 64 + 16 * t4; k < a.K + 16 * t4; k += warps * 64) {
+    const uint4 p = load_weight16(wa, k, a.K, !GATED && ra == a.N - 1);
+    const uint4 q = load_weight16(wb, k, a.K, rb == (GATED ? 2 * a.N : a.N) - 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) product(n, p, q, load_x(n, k, false));
   }
@@ -252,26 +248,31 @@ cudaError_t start_few(const LinArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, few_kernel<NT, U, GATED, HALF>, a);
 }
 
+long long few_ctas(const LinArgs& a, bool gated) { return ((long long)a.N + (gated ? 7 : 15)) / (gated ? 8 : 16); }
+
 template <bool GATED>
 int launch_few(const LinArgs& a, cudaStream_t s) {
   const cudaError_t e = a.T <= 8    ? start_few<1, 2, GATED, false>(a, s)
                         : a.T <= 16 ? start_few<2, 2, GATED, false>(a, s)
-                        : a.T <= 32 ? start_few<4, 2, GATED, false>(a, s)
-                                    : start_few<8, 2, GATED, false>(a, s);
+                        : a.T > 32  ? start_few<8, 1, GATED, false>(a, s)
+                        : few_ctas(a, GATED) <= 296 ? start_few<4, 2, GATED, false>(a, s)
+                                                    : start_few<4, 1, GATED, false>(a, s);
   return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
-// few_kernel or the tensor cores' kernels (one launch of those is 4 us longer,
+// few_kernel or the tensor cores' kernels (one launch of those is 3 us longer,
 // and their time grows less with tokens): up to 16 tokens always; to 64 where
 // the tokens' rows, which every CTA reads, are short and the CTAs fit the card
-// at once (two an SM up to 32 tokens, one beyond).  Measured, us, few_kernel
-// and mid_kernel: 32 tokens, N = K = 2048 4.2 and 7.6; N = 6144, K = 2048 9.1
-// and 8.4; 64 tokens, N = K = 2048 6.5 and 8.3; N = 2048, K = 4096 9.0 and 8.7;
-// N = 6144, K = 512 9.6 and 8.4.
+// at once (three an SM with one segment at a time or two up to 32 tokens, one
+// beyond).  Measured, us, few_kernel and mid_kernel: 32 tokens, N = K = 2048 3.7
+// and 7.6; N = 6144, K = 512 3.9 and 5.2; N = K = 6144 13.8 and 12.1; 64 tokens,
+// N = K = 2048 5.8 and 7.6; N = 2048, K = 4096 9.6 and 7.9; N = 6144, K = 512
+// 8.3 and 6.3.
 bool few_tokens(const LinArgs& a, bool gated) {
   if (a.T <= kFewTokens) return true;
-  const long long ctas = ((long long)a.N + (gated ? 7 : 15)) / (gated ? 8 : 16);
-  return a.T <= 64 && (long long)a.T * a.K <= 131072 && ctas <= (a.T <= 32 ? 296 : 148);
+  const long long ctas = few_ctas(a, gated), rows = (long long)a.T * a.K;
+  if (a.T <= 32) return rows <= (ctas <= 296 ? 131072 : 32768) && ctas <= 444;
+  return a.T <= 64 && rows <= 131072 && ctas <= 148;
 }
 
 int launch_linear(const LinArgs& a, bool gated, cudaStream_t s) {
