@@ -117,8 +117,8 @@ __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, 
 // memory to the registers of the MMA with no stop: lane (g, t) holds 16 bytes
 // of rows g and g + 8 at byte 16 t of each half of a segment, which are the A
 // operands of two MMAs once K is permuted the same way in the tokens' rows.
-// The loads of U segments are under way before the first product, and the
-// first ones before the kernel in front is done (weights do not depend on it).
+// The loads of U segments are under way before the first product, and in a
+// chain the first ones before the kernel in front is done.
 // HALF: the tokens are bf16 rows (the MLP's h), which every CTA brings to codes
 // itself, in shared memory: T * K is small, and a launch is saved.
 // Measured, N = K = 6144 from memory: 1 token 8.0 us (4.7 TB/s with the launch),
@@ -165,9 +165,10 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
   };
   int sg = warp;
   const bool some = sg + (U - 1) * warps < full;
-  if (some) load_w(sg);
+  if (some && a.chained) load_w(sg);
   pdl_wait();
   pdl_trigger();
+  if (some && !a.chained) load_w(sg);
   if (HALF) {
     few_codes(a, s_x, pitch, s_xs);
     __syncthreads();
@@ -244,7 +245,7 @@ cudaError_t start_few(const LinArgs& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = 8 * 8 * NT * 16 * 4 + (HALF ? 8 * NT * few_pitch(a.K) : 0);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.chained;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, few_kernel<NT, U, GATED, HALF>, a);
 }
 
@@ -374,6 +375,7 @@ extern "C" int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long l
     dn.ldx = o.ldh;
     return start_few<1, 2, false, true>(dn, s) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
   }
-  rc = q4_launch_quant_chained(p + o.h, o.ldh, T, mlp->I, (int8_t*)(p + o.q), o.ldq, (float*)(p + o.scale), s);
+  rc = moe_q4_quant_rows(p + o.h, MOE_Q4_BF16, o.ldh, T, mlp->I, (int8_t*)(p + o.q), o.ldq, (float*)(p + o.scale),
+                         stream);
   return rc == MOE_Q4_OK ? launch_linear(dn, false, s) : rc;
 }

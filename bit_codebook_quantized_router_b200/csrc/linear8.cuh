@@ -6,6 +6,11 @@
 
 namespace q4 {
 
+// Every kernel of the int8 calls lets the next one of the stream start early
+// and waits itself, before its first access, for the kernels in front
+// (griddepcontrol): launches and prologues overlap.  Only in a chain inside one
+// call are weights read before that wait, since elsewhere the kernel in front
+// may be the one that writes them.
 struct LinArgs {
   const int8_t* x;       // [T][ldx]
   const float* xs;       // [T]
@@ -17,8 +22,7 @@ struct LinArgs {
   long long ldx, ldw, ldo;
   int T, N, K;
   int out_f32;
-  int chained;           // launched behind a kernel of the same call that lets it start early: the weights
-                         // may be read at once, x and xs after griddepcontrol.wait
+  int chained;           // behind a kernel of the same call: the weights may be read before it is done
 };
 
 // The one place that turns a sum into a value: the same bits in every kernel.

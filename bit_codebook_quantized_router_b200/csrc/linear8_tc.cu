@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kThreads)
     fence_mbar_init();
     // the ring's first loads, before anything is set up beside them; in a
     // chain the weights' before the kernel in front is done with the tokens
+    if (!a.chained) pdl_wait();
     for (int i = 0; i < S && k_lo + i < k_hi; ++i) {
       load_w(k_lo + i, i);
       if (!a.chained) load_x(k_lo + i, i);
@@ -371,6 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true, filled = !a.chained;
+      if (!a.chained) pdl_wait();
       for (int tile = first; tile < total && ok; tile += step) {
         const int m = tile % m_tiles, n = tile / m_tiles;
         const int ya = m * 256 + rank * 128;
@@ -586,7 +588,7 @@ int launch_mid(const LinArgs& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.chained ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, mid_kernel<GATED>, a, p, tx, tw) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
@@ -613,7 +615,7 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = kWideSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.chained;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, tx, tw) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 

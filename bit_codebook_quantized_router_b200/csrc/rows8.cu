@@ -31,19 +31,16 @@ struct RowArgs {
   float* scale;
   long long ldx, ldr, ldro, ldo, ldq;
   int T, H;
-  int chained;          // launched behind a kernel of the same call that lets it start early
   int weight_f32;
   int exact;            // the values' products with the weight have 16-bit significands
   float eps;
 };
 
-// In a chain the next kernel may start at once (it waits itself before it
-// reads this one's rows), and this one waits for the rows it reads.
-__device__ __forceinline__ void begin(const RowArgs& a) {
-  if (a.chained) {
-    pdl_trigger();
-    pdl_wait();
-  }
+// The stream's next kernel may start at once (those that read these results
+// wait themselves), and this one waits for the kernels in front.
+__device__ __forceinline__ void begin() {
+  pdl_trigger();
+  pdl_wait();
 }
 
 template <typename K>
@@ -57,7 +54,7 @@ cudaError_t start(K kernel, const RowArgs& a, long long grid, int threads, int s
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.chained;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -294,7 +291,7 @@ __device__ __forceinline__ void reduce(float& m, float& sum, int buf) {
 template <bool RES, bool NORM, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ? 8 : 1024 / THREADS)
     row_kernel(const __grid_constant__ RowArgs a) {
-  begin(a);
+  begin();
   typedef __nv_bfloat16 bf;
   constexpr bool kWarp = THREADS == 32;
   constexpr int kCta = kWarp ? 128 : THREADS;
@@ -352,7 +349,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ?
 // where one row's latency counts, and rows of fp32.
 template <typename XT, typename RT, bool NORM, int NV>
 __global__ void __launch_bounds__(1024) direct_row_kernel(const __grid_constant__ RowArgs a) {
-  begin(a);
+  begin();
   const long long row = blockIdx.x;
   float p[NV][8];
   float sum = 0.0f, m = 0.0f;
@@ -382,6 +379,7 @@ __global__ void __launch_bounds__(1024) direct_row_kernel(const __grid_constant_
 // Rows on other boundaries, value by value: a CTA a row, NV values a thread.
 template <typename XT, typename RT, bool NORM, int NV>
 __global__ void __launch_bounds__(1024) odd_row_kernel(const __grid_constant__ RowArgs a) {
+  begin();
   const long long row = blockIdx.x;
   float p[NV][1];
   float sum = 0.0f, m = 0.0f;
@@ -408,7 +406,7 @@ __global__ void __launch_bounds__(1024) odd_row_kernel(const __grid_constant__ R
 // first, so out may be x and res_out may be res or x.
 template <typename XT, typename RT, bool NORM>
 __global__ void __launch_bounds__(1024) row_loop_kernel(const __grid_constant__ RowArgs a) {
-  begin(a);
+  begin();
   const long long row = blockIdx.x;
   float sum = 0.0f, m = 0.0f;
   for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
@@ -535,15 +533,6 @@ extern "C" int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T
   const cudaStream_t s = (cudaStream_t)stream;
   return x_type == MOE_Q4_F32 ? launch<float, NoRes, false>(a, vec, s)
                               : launch<__nv_bfloat16, NoRes, false>(a, vec, s);
-}
-
-int q4_launch_quant_chained(const void* x, long long ldx, int T, int K, int8_t* q, long long ldq, float* scale,
-                            cudaStream_t s) {
-  RowArgs a = {};
-  a.x = x, a.ldx = ldx;
-  a.q = q, a.ldq = ldq, a.scale = scale;
-  a.T = T, a.H = K, a.exact = 1, a.chained = 1;
-  return launch<__nv_bfloat16, NoRes, false>(a, aligned(x, ldx, 2, 16) && aligned(q, ldq, 1, 8), s);
 }
 
 extern "C" int moe_q4_add_norm(const void* x, int x_type, long long ldx, const void* residual, int residual_type,

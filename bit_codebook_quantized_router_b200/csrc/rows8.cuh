@@ -156,7 +156,3 @@ __device__ __forceinline__ void unpack(uint4 a, float v[8]) {
 }
 
 }  // namespace q4
-
-// moe_q4_quant_rows behind a kernel of the same call that lets it start early.
-int q4_launch_quant_chained(const void* x, long long ldx, int T, int K, int8_t* q, long long ldq, float* scale,
-                            cudaStream_t s);
