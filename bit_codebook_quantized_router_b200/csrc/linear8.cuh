@@ -10,7 +10,8 @@ namespace q4 {
 // and waits itself, before its first access, for the kernels in front
 // (griddepcontrol): launches and prologues overlap.  Only in a chain inside one
 // call are weights read before that wait, since elsewhere the kernel in front
-// may be the one that writes them.
+// may be the one that writes them; so a product lets the next one start only
+// after its own wait, when what was in front of the call is done.
 struct LinArgs {
   const int8_t* x;       // [T][ldx]
   const float* xs;       // [T]

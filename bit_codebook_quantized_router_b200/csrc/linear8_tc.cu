@@ -358,7 +358,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
-  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
 
   const int m_tiles = (a.T + 255) / 256;
@@ -432,6 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, e = threadIdx.x - 32 * kEpiWarp0;
     const int align = out_align(a);
     pdl_wait();
+    pdl_trigger();  // (after the wait: the next kernels of a chain read weights at once)
     float* stage = s_rows + (warp - kEpiWarp0) * 32 * kWideRow;
     uint32_t use = 0;
     bool lost = false;

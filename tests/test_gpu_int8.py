@@ -459,3 +459,35 @@ def test_two_threads_on_two_streams():
     [t.start() for t in ts]
     [t.join() for t in ts]
     assert not bad
+
+
+@pytest.mark.parametrize("T", [1, 6, 40, 300])
+def test_operands_written_just_before(T):
+    # every operand of the calls is rewritten by the kernels right in front of
+    # them, with no wait between: launches overlap, results may not
+    H, I = 2048, 1024
+    gus = [(0.05 * torch.randn((2 * I, H), generator=gen(i))).to(BF).cuda() for i in range(3)]
+    dns = [(0.05 * torch.randn((H, I), generator=gen(9 + i))).to(BF).cuda() for i in range(3)]
+    xs = [rows(T, H, 20 + i).cuda() for i in range(3)]
+    gu, dn = q4.quant_rows(gus[0]), q4.quant_rows(dns[0])
+    m = q4.MlpI8(*gu, *dn)
+    q, s = q4.quant_rows(xs[0])
+    ws = q4.alloc_workspace(q4.mlp_i8_workspace(m, T))
+
+    def step(i):
+        q4.quant_rows(xs[i], q=q, scale=s)
+        q4.quant_rows(gus[i], q=gu[0], scale=gu[1])
+        y = q4.linear_i8(q, s, gu[0], gu[1])
+        r, h, _, _ = q4.add_norm(y[:, :H].contiguous(), None, residual=xs[i], q=q, scale=s)
+        q4.quant_rows(dns[i], q=dn[0], scale=dn[1])
+        return y, h, q4.mlp_i8(m, q, s, ws=ws)
+
+    want = []
+    for i in range(3):
+        want.append([t.clone() for t in step(i)])
+        torch.cuda.synchronize()
+    got = [step(i % 3) for i in range(30)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for a, b in zip(want[i % 3], out):
+            assert torch.equal(a, b)
