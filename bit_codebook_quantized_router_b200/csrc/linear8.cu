@@ -278,7 +278,11 @@ bool few_tokens(const LinArgs& a, bool gated) {
 
 int launch_linear(const LinArgs& a, bool gated, cudaStream_t s) {
   if (few_tokens(a, gated)) return gated ? launch_few<true>(a, s) : launch_few<false>(a, s);
-  if (a.T <= kLinearMidTokens) return q4_launch_linear_mid(a, gated, s);
+  // mid_kernel's K over a cluster, or wide_kernel's pairs: to 64 tokens always
+  // the first, to 128 where K is long.  Measured at 96 tokens, us, mid_kernel
+  // and wide_kernel: N = K = 6144 15.2 and 18.0; N = 512, K = 6144 7.8 and 16.5;
+  // N = 1003, K = 1990 6.5 and 9.2; N = K = 600 6.2 and 5.3.
+  if (a.T <= 64 || (a.T <= kLinearMidTokens && a.K >= 1536)) return q4_launch_linear_mid(a, gated, s);
   return q4_launch_linear_wide(a, gated, s);
 }
 

@@ -42,4 +42,4 @@ __device__ __forceinline__ void store_out(const LinArgs& a, long long t, int n, 
 // tokens (K split over a cluster) and for many (CTA pairs).
 int q4_launch_linear_mid(const q4::LinArgs& a, bool gated, cudaStream_t s);
 int q4_launch_linear_wide(const q4::LinArgs& a, bool gated, cudaStream_t s);
-constexpr int kLinearMidTokens = 64;  // the most that q4_launch_linear_mid takes
+constexpr int kLinearMidTokens = 128;  // the most that q4_launch_linear_mid takes

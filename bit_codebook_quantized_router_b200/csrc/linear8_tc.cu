@@ -1,9 +1,10 @@
 // Int8 products on the 5th-generation tensor cores (tcgen05, kind::i8, int32
 // accumulators in TMEM), for moderate and large numbers of tokens.
 //
-// mid_kernel, up to 64 tokens: the weights' bytes bound it.  The MMA's M is 128
+// mid_kernel, up to 128 tokens: the weights' bytes bound it.  The MMA's M is 128
 // weight rows and its N all the tokens, so each weight is read once; K is split
-// over the CTAs of a cluster, two CTAs an SM, so that every SM streams weights.
+// over the CTAs of a cluster, two CTAs an SM to 64 tokens, so that every SM
+// streams weights.
 // The partial sums are int32, so adding them is exact in any order: each CTA
 // sends the columns that another owns to that CTA's shared memory, and each
 // finishes its own columns.  No workspace and one launch.  Measured, N = K =
@@ -67,7 +68,7 @@ __device__ __forceinline__ void give_up(int32_t* status, uint64_t* full, int sta
     }
 }
 
-// ---- up to 64 tokens ------------------------------------------------------------
+// ---- up to 128 tokens -----------------------------------------------------------
 
 struct MidPlan {
   int bn;       // tokens, rounded up to 16
@@ -557,21 +558,26 @@ int launch_mid(const LinArgs& a, cudaStream_t s) {
   p.bn = (a.T + 15) / 16 * 16;
   p.ksteps = (a.K + kBK - 1) / kBK;
   const int tiles = GATED ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  const int sms = sm_count();
-  // K split in two, four or eight while the CTAs fit the card at two an SM
-  // (clusters leave an eighth of them unused) and keep two k-steps
+  const int stage = kTile + p.bn * kBK;
+  // two CTAs an SM where their rings and inboxes fit (to 64 tokens), else one
+  const int an_sm = p.bn <= 64 ? 2 : 1, room = an_sm == 2 ? 108 * 1024 : 216 * 1024;
+  // K split in two, four or eight while the CTAs fit the card at once (clusters
+  // leave an eighth of it unused, at one CTA an SM those of eight a fifth) and
+  // keep two k-steps
+  const long long slots = an_sm * sm_count();
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 2 * sms * 7 / 8 && p.ksteps >= 4 * splits) splits *= 2;
+  while (splits < 8 && 2ll * splits * tiles <= (splits == 4 && an_sm == 1 ? slots * 4 / 5 : slots * 7 / 8) && p.ksteps >= 4 * splits)
+    splits *= 2;
   p.own = (p.bn / 8 + splits - 1) / splits * 8;
-  const int stage = kTile + p.bn * kBK, most = (p.ksteps + splits - 1) / splits, box = splits * p.own * 512;
-  p.stages = min(min(most, kMidStages), (108 * 1024 - box) / stage);
+  const int most = (p.ksteps + splits - 1) / splits, box = splits * p.own * 512;
+  p.stages = min(min(most, kMidStages), (room - box) / stage);
   p.inbox = p.stages * stage;
   const int smem = p.inbox + box + 1024;
   CUtensorMap tx, tw;
   if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, p.bn) ||
       !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, GATED ? 64 : 128))
     return MOE_Q4_ECUDA;
-  if (cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) !=
+  if (cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
           cudaSuccess ||
       cudaFuncSetAttribute(mid_kernel<GATED>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return MOE_Q4_ECUDA;
