@@ -126,7 +126,7 @@ __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, 
 // Three CTAs an SM (85 registers): with two, 384 CTAs take two turns (9.2 us).
 template <int NT, int U, bool GATED, bool HALF>
 __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {
-  extern __shared__ int s_acc[];  // [warps][8 NT][16]; HALF: and codes [8 NT][pitch] behind
+  extern __shared__ int s_acc[];  // [warps][8 NT][16]; HALF: and codes [T][pitch] behind
   __shared__ float s_xs[8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -242,7 +242,7 @@ cudaError_t start_few(const LinArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 8 * 8 * NT * 16 * 4 + (HALF ? 8 * NT * few_pitch(a.K) : 0);
+  cfg.dynamicSmemBytes = 8 * 8 * NT * 16 * 4 + (HALF ? a.T * few_pitch(a.K) : 0);  // (codes of real tokens only)
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

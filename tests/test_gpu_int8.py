@@ -374,6 +374,18 @@ def test_mlp(T, H, I, dtype):
     assert torch.equal(got.clone(), q4.mlp_i8(m, q, s, dtype=dtype, ws=ws.view))
 
 
+@pytest.mark.parametrize("T,I", [(1, 5400), (1, 5600), (1, 8192), (1, 8193), (2, 4096), (2, 4097), (3, 2730), (4, 2048),
+                                 (5, 1638), (7, 1170), (8, 1024), (8, 1025)])
+def test_mlp_few_tokens_of_long_rows(T, I):
+    # both sides of the limit to which the down product makes h's codes itself
+    m = mlp_weights(40, I, I)
+    q, s = q4.quant_rows(rows(T, 40, T, spread=False).cuda())
+    got = q4.mlp_i8(m, q, s, dtype=F)
+    check_mlp(got, m, q.cpu(), s.cpu())
+    for t in range(T):
+        assert torch.equal(q4.mlp_i8(m, q[t:t + 1], s[t:t + 1], dtype=F), got[t:t + 1])
+
+
 def test_mlp_rows_are_independent():
     m = mlp_weights(512, 272, 5)
     q, s = q4.quant_rows(rows(400, 512, 6).cuda())
