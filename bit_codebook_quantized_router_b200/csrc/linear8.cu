@@ -121,8 +121,8 @@ __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, 
 // chain the first ones before the kernel in front is done.
 // HALF: the tokens are bf16 rows (the MLP's h), which every CTA brings to codes
 // itself, in shared memory: T * K is small, and a launch is saved.
-// Measured, N = K = 6144 from memory: 1 token 8.0 us (4.7 TB/s with the launch),
-// 8 tokens 8.9, 16 tokens 12.9; the memory's bandwidth and the launch bound it.
+// Measured, N = K = 6144 from memory: 1 token 7.8 us (4.8 TB/s with the launch),
+// 8 tokens 8.3, 16 tokens 9.7; the memory's bandwidth and the launch bound it.
 // Three CTAs an SM (85 registers): with two, 384 CTAs take two turns (9.2 us).
 template <int NT, int U, bool GATED, bool HALF>
 __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {

@@ -8,9 +8,9 @@
 // The partial sums are int32, so adding them is exact in any order: each CTA
 // sends the columns that another owns to that CTA's shared memory, and each
 // finishes its own columns.  No workspace and one launch.  Measured, N = K =
-// 6144 from memory: 17 tokens 11.5 us, 64 tokens 13.3 (2.9 TB/s with the
-// launch): weights arrive from 2.4 to 8.7 us of it at 6.3 TB/s, the exchange and
-// the last step take 4.  With the weights as the MMA's N = 256 and the tokens as
+// 6144 from memory: 17 tokens 10.5 us, 64 tokens 12.4 (3.1 TB/s with the
+// launch), 128 tokens 16.4.  At 64 the weights arrive from 2.4 to 8.5-10 us of a
+// CTA's life, the exchange and the last step take 3.  With the weights as the MMA's N = 256 and the tokens as
 // its M, 64 tokens took 22 us: twice the sums to exchange, by half the warps.
 //
 // wide_kernel, more tokens: pairs of CTAs (cta_group::2) multiply 256 tokens
@@ -19,9 +19,9 @@
 // two accumulators, so that one tile's results leave while the next is
 // multiplied.  An MMA of 256 x 256 x 32 takes 129 cycles (128 is the units'
 // rate); one of a single CTA, 128 rows, takes 170 whatever its N.  Measured:
-// 8192 tokens, N = K = 6144 200 us, 3.09 POP/s (1.88 times the measured bf16
-// rate; the tensor pipe is busy 85% of the time that SMs are, at 1.66 GHz under
-// the power limit); 2048 tokens 54 us; 256 tokens, K = 2048 11.2 us.  A tile's
+// 8192 tokens, N = K = 6144 200 us, 3.1 POP/s (1.88 times the measured bf16
+// rate; at 4096 tokens, 102 us, the tensor pipe is busy 85% of the time that SMs
+// are); 2048 tokens 53 us; 256 tokens, K = 2048 9.6-9.9 us.  A tile's
 // results take 4 us to leave, hidden but for the last tile's; staging them in
 // shared memory for whole lines or for TMA stores was no faster end to end
 // (2048 tokens, K = 2048: 23.6 us as it is, 25.2 to 26.0 so).
@@ -49,7 +49,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kEpiWarp0 = 2;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSmemExtra = 2048;       // alignment and barriers
 constexpr int kMidStages = 8;
 
@@ -85,9 +84,10 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[kMidStages], empty[kMidStages], acc_full[1], in_full[1];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word;
+  __shared__ int abort_word, in_abort_word;
   __shared__ float s_xs[kLinearMidTokens];
   volatile int* abort_flag = &abort_word;
+  volatile int* in_abort = &in_abort_word;
   uint8_t* smem = align1024(smem_raw);
   const int S = p.stages, b_tile = p.bn * kBK;
   uint8_t* sA = smem;              // [S][128][128 B] weights
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     mbar_init(acc_full, 1);
     mbar_init(in_full, splits * kEpiWarps);
-    *abort_flag = 0;
+    *abort_flag = *in_abort = 0;
     fence_mbar_init();
     // the ring's first loads, before anything is set up beside them; in a
     // chain the weights' before the kernel in front is done with the tokens
@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_before();
 
     // finish this CTA's columns, four at a time, once all their sums are here
-    mbar_wait_warp<true>(in_full, 0, abort_flag, kWaitNs);
+    // (a CTA that gave a wait up sends too, after give_up; so this one is longer
+    // than that takes and has a flag of its own: no CTA ends while another sends)
+    if (!mbar_wait_warp<true>(in_full, 0, in_abort, 3 * kWaitNs)) *abort_flag = 1;
     if (n < a.N) {
       constexpr int kStep = 32 * kEpiWarps / kRows;
       const uint32_t box = inbox + (et & (kRows - 1)) * 4;

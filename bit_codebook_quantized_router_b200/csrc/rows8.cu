@@ -285,9 +285,9 @@ __device__ __forceinline__ void reduce(float& m, float& sum, int buf) {
 // to shared memory (cp.async, each thread to slots of its own) while this one
 // is reduced and written: the card's bandwidth needs more bytes under way than
 // the registers of a row in work leave room for.  Measured at 8192 rows of
-// 6144, residual and norm: 76 us (5.96 TB/s), rows read into registers with
+// 6144, residual and norm: 76 us (5.9 TB/s), rows read into registers with
 // nothing ahead 99 us; two to four rows ahead 75 to 82 us.  4096 rows of 6144
-// to codes alone: 15.8 us against 21.8.
+// to codes alone: 15.3 us against 21.8.
 template <bool RES, bool NORM, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS == 32 ? 8 : 1024 / THREADS)
     row_kernel(const __grid_constant__ RowArgs a) {

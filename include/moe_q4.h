@@ -448,6 +448,7 @@ MOE_Q4_API int moe_q4_combine(const float* y, const float* w, const int32_t* inv
  *   T >= 0; 1 <= K <= 2^30 (MOE_Q4_ENOTSUP above);
  *   q      device int8 [T][ldq] (out);  scale  device fp32 [T] (out).
  * The codes are exact as defined above; scale is one fp32 division.
+ * q and scale overlap neither x nor each other (undefined otherwise).
  * Alignment of x and q is that of their elements; 16-byte (x) and 8-byte (q)
  * bases and row strides take the faster vector path.  No workspace. */
 MOE_Q4_API int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T, int K, int8_t* q, long long ldq,
