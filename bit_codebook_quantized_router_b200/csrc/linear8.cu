@@ -8,7 +8,6 @@
 // split.  The one rounding of a sum is its conversion to fp32; the product of
 // the scales and the result's are one each, and the result's type is the last.
 #include "linear8.cuh"
-#include "rows8.cuh"
 
 namespace q4 {
 
@@ -25,66 +24,6 @@ __device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint3
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Bytes of a token's codes in shared memory: whole segments, and rows half a
-// line apart so that eight lanes of two rows meet no bank twice.
-__host__ __device__ constexpr int few_pitch(int K) { return (K + 127) / 128 * 128 + 64; }
-
-// The T bf16 rows at a.x as codes (zeros past K): 8 / T warps a row (T rounded
-// up to a power of two), the row's maximum by shared atomics (magnitudes
-// compare as their bits do, and a maximum does not depend on the order).
-__device__ __forceinline__ void few_codes(const LinArgs& a, int8_t* s_x, int pitch, float* s_xs) {
-  __shared__ uint32_t s_m[8];
-  constexpr int kKeep = 4;  // vectors of 8 values that stay in registers between the passes
-  const int share = a.T <= 1 ? 8 : a.T <= 2 ? 4 : a.T <= 4 ? 2 : 1;  // warps a row
-  const int t = (threadIdx.x >> 5) / share, step = 32 * share, first = threadIdx.x - t * step;
-  const int vectors = (pitch - 64) / 8;
-  const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(a.x) + t * a.ldx;  // (ldx: a multiple of 8)
-  auto read = [&](int i) { return i < a.K ? *reinterpret_cast<const uint4*>(row + i) : make_uint4(0, 0, 0, 0); };
-  auto values = [&](uint4 w, int i, float v[8]) {
-    unpack(w, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j >= a.K) v[j] = 0.0f;
-  };
-  auto largest = [&](float m, uint4 w, int i) {
-    float v[8];
-    values(w, i, v);
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) m = max_abs(m, v[j], v[j + 1]);
-    return m;
-  };
-  if (threadIdx.x < 8) s_m[threadIdx.x] = 0;
-  __syncthreads();
-  uint4 keep[kKeep];
-  float m = 0.0f;
-  if (t < a.T) {
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u) keep[u] = read((first + u * step) * 8);
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u) m = largest(m, keep[u], (first + u * step) * 8);
-    for (int v = first + kKeep * step; v < vectors; v += step) m = largest(m, read(v * 8), v * 8);
-    m = warp_max(m);
-    if ((threadIdx.x & 31) == 0) atomicMax(&s_m[t], __float_as_uint(m));
-  }
-  __syncthreads();
-  if (t < a.T) {
-    const RowScale s = row_scale(__uint_as_float(s_m[t]), 0.0f, false, a.K, 0.0f);
-    if (first == 0) s_xs[t] = s.scale;
-    auto put = [&](uint4 w, int i) {
-      float v[8];
-      uint32_t c[8];
-      values(w, i, v);
-      ready<8>(v, s);
-      codes<8>(v, s, true, c);
-      *reinterpret_cast<uint2*>(s_x + t * pitch + i) = pack_codes(c);
-    };
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u)
-      if (first + u * step < vectors) put(keep[u], (first + u * step) * 8);
-    for (int v = first + kKeep * step; v < vectors; v += step) put(read(v * 8), v * 8);
-  }
 }
 
 // The first n (1 to 15) bytes at p (16-byte aligned), and zeros.
@@ -119,15 +58,12 @@ __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, 
 // operands of two MMAs once K is permuted the same way in the tokens' rows.
 // The loads of U segments are under way before the first product, and in a
 // chain the first ones before the kernel in front is done.
-// HALF: the tokens are bf16 rows (the MLP's h), which every CTA brings to codes
-// itself, in shared memory: T * K is small, and a launch is saved.
 // Measured, N = K = 6144 from memory: 1 token 7.8 us (4.8 TB/s with the launch),
 // 8 tokens 8.3, 16 tokens 9.7; the memory's bandwidth and the launch bound it.
 // Three CTAs an SM (85 registers): with two, 384 CTAs take two turns (9.2 us).
-template <int NT, int U, bool GATED, bool HALF>
+template <int NT, int U, bool GATED>
 __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {
-  extern __shared__ int s_acc[];  // [warps][8 NT][16]; HALF: and codes [T][pitch] behind
-  __shared__ float s_xs[8 * NT];
+  extern __shared__ int s_acc[];  // [warps][8 NT][16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int n0 = blockIdx.x * (GATED ? 8 : 16);
@@ -136,14 +72,11 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
   const int8_t* wa = a.w + ra * a.ldw;
   const int8_t* wb = a.w + rb * a.ldw;
   const int full = a.K / 128;  // whole segments
-  const int pitch = few_pitch(a.K);
-  int8_t* const s_x = reinterpret_cast<int8_t*>(s_acc + warps * 8 * NT * 16);
   int acc[NT][4] = {};
 
   auto load_x = [&](int n, int k, bool whole) {
     const int t = 8 * n + g;
     if (t >= a.T) return make_uint4(0, 0, 0, 0);
-    if (HALF) return *reinterpret_cast<const uint4*>(s_x + t * pitch + k);
     // (no read-only path: in a chain the rows are written while this kernel runs)
     if (whole) return *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
     return load_row16(a.x + t * a.ldx, k, a.K);
@@ -169,10 +102,6 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
   pdl_wait();
   pdl_trigger();
   if (some && !a.chained) load_w(sg);
-  if (HALF) {
-    few_codes(a, s_x, pitch, s_xs);
-    __syncthreads();
-  }
   if (some)
     for (;;) {
       uint4 x[U][2][NT];
@@ -224,7 +153,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
       v += s_acc[(w * 8 * NT + t) * 16 + r];
       if (GATED) u += s_acc[(w * 8 * NT + t) * 16 + r + 8];
     }
-    const float xs = HALF ? s_xs[t] : a.xs[t];
+    const float xs = a.xs[t];
     float y = scaled(v, xs, a.ws[n]);
     if (GATED)
       y = silu_mul_fast(y, scaled(u, xs, a.ws[a.N + n]));
@@ -234,7 +163,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
   }
 }
 
-template <int NT, int U, bool GATED, bool HALF>
+template <int NT, int U, bool GATED>
 cudaError_t start_few(const LinArgs& a, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -242,22 +171,22 @@ cudaError_t start_few(const LinArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 8 * 8 * NT * 16 * 4 + (HALF ? a.T * few_pitch(a.K) : 0);  // (codes of real tokens only)
+  cfg.dynamicSmemBytes = 8 * 8 * NT * 16 * 4;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<NT, U, GATED, HALF>, a);
+  return cudaLaunchKernelEx(&cfg, few_kernel<NT, U, GATED>, a);
 }
 
 long long few_ctas(const LinArgs& a, bool gated) { return ((long long)a.N + (gated ? 7 : 15)) / (gated ? 8 : 16); }
 
 template <bool GATED>
 int launch_few(const LinArgs& a, cudaStream_t s) {
-  const cudaError_t e = a.T <= 8    ? start_few<1, 2, GATED, false>(a, s)
-                        : a.T <= 16 ? start_few<2, 2, GATED, false>(a, s)
-                        : a.T > 32  ? start_few<8, 1, GATED, false>(a, s)
-                        : few_ctas(a, GATED) <= 296 ? start_few<4, 2, GATED, false>(a, s)
-                                                    : start_few<4, 1, GATED, false>(a, s);
+  const cudaError_t e = a.T <= 8    ? start_few<1, 2, GATED>(a, s)
+                        : a.T <= 16 ? start_few<2, 2, GATED>(a, s)
+                        : a.T > 32  ? start_few<8, 1, GATED>(a, s)
+                        : few_ctas(a, GATED) <= 296 ? start_few<4, 2, GATED>(a, s)
+                                                    : start_few<4, 1, GATED>(a, s);
   return e == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
@@ -285,12 +214,6 @@ int launch_linear(const LinArgs& a, bool gated, cudaStream_t s) {
   if (a.T <= 64 || (a.T <= kLinearMidTokens && a.K >= 1536)) return q4_launch_linear_mid(a, gated, s);
   return q4_launch_linear_wide(a, gated, s);
 }
-
-// The MLP's down product takes h itself, without a launch for its codes, where
-// making them in every CTA takes little time.  Measured at H = 6144, I = 2048:
-// 1 token 12.0 us in two launches, 14.5 in three; 4 tokens 13.0; 8 tokens 15.5
-// in two, 14.4 in three.
-bool down_from_half(int T, int I) { return T <= 8 && (long long)T * I <= 8192; }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -372,13 +295,11 @@ extern "C" int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long l
                       o.ldh, T, mlp->I, mlp->H, 0};
   rc = launch_linear(gu, true, s);
   if (rc != MOE_Q4_OK) return rc;
-  LinArgs dn = {(const int8_t*)(p + o.q), (const float*)(p + o.scale), mlp->down, mlp->down_scale, nullptr, out,
-                status, o.ldq, mlp->ld_down, ldo, T, mlp->H, mlp->I, out_type == MOE_Q4_F32, 1};
-  if (down_from_half(T, mlp->I)) {
-    dn.x = (const int8_t*)(p + o.h);
-    dn.ldx = o.ldh;
-    return start_few<1, 2, false, true>(dn, s) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
-  }
+  const LinArgs dn = {(const int8_t*)(p + o.q), (const float*)(p + o.scale), mlp->down, mlp->down_scale, nullptr, out,
+                     status, o.ldq, mlp->ld_down, ldo, T, mlp->H, mlp->I, out_type == MOE_Q4_F32, 1};
+  // h's codes in a launch of their own also for few tokens: 9.6 us in three
+  // launches (8 tokens, H = 6144, I = 512), 10.5 with every CTA of the down
+  // product making them itself; 1 token, I = 2048 11.6 and 11.75
   rc = moe_q4_quant_rows(p + o.h, MOE_Q4_BF16, o.ldh, T, mlp->I, (int8_t*)(p + o.q), o.ldq, (float*)(p + o.scale),
                          stream);
   return rc == MOE_Q4_OK ? launch_linear(dn, false, s) : rc;

@@ -377,7 +377,7 @@ def test_mlp(T, H, I, dtype):
 @pytest.mark.parametrize("T,I", [(1, 5400), (1, 5600), (1, 8192), (1, 8193), (2, 4096), (2, 4097), (3, 2730), (4, 2048),
                                  (5, 1638), (7, 1170), (8, 1024), (8, 1025)])
 def test_mlp_few_tokens_of_long_rows(T, I):
-    # both sides of the limit to which the down product makes h's codes itself
+    # rows of h to 8192 values and past them, for few tokens
     m = mlp_weights(40, I, I)
     q, s = q4.quant_rows(rows(T, 40, T, spread=False).cuda())
     got = q4.mlp_i8(m, q, s, dtype=F)
