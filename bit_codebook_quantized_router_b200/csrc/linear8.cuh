@@ -27,7 +27,11 @@ struct LinArgs {
 };
 
 // The one place that turns a sum into a value: the same bits in every kernel.
-__device__ __forceinline__ float scaled(int acc, float xs, float ws) { return (float)acc * (xs * ws); }
+// (__fmul_rn: a product that is not contracted with a bias behind it, as the
+// two-at-a-time products of wide_kernel are not)
+__device__ __forceinline__ float scaled(int acc, float xs, float ws) {
+  return __fmul_rn((float)acc, __fmul_rn(xs, ws));
+}
 
 __device__ __forceinline__ void store_out(const LinArgs& a, long long t, int n, float v) {
   if (a.out_f32)

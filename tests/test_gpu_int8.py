@@ -280,6 +280,17 @@ def test_linear_rows_are_independent_and_repeat():
         assert torch.equal(q4.linear_i8(xg[lo:hi], xsg[lo:hi], wg, wsg, dtype=F), full[lo:hi])
 
 
+@pytest.mark.parametrize("N,K", [(515, 1000), (515, 2000), (130, 100)])
+def test_linear_rows_with_bias_are_independent(N, K):
+    x, xs = int8_rows(700, K, 1)
+    w, ws = int8_rows(N, K, 2)
+    b = torch.randn(N, generator=gen(3)).cuda()
+    xg, xsg, wg, wsg = on_gpu(x), xs.cuda(), on_gpu(w), ws.cuda()
+    full = q4.linear_i8(xg, xsg, wg, wsg, bias=b, dtype=F)
+    for lo, hi in ((0, 1), (3, 10), (100, 113), (200, 233), (300, 400), (0, 250), (90, 600)):
+        assert torch.equal(q4.linear_i8(xg[lo:hi], xsg[lo:hi], wg, wsg, bias=b, dtype=F), full[lo:hi])
+
+
 def test_linear_empty_and_refusals():
     w, ws = q4.quant_rows(rows(8, 32, 1, spread=False).cuda())
     x = torch.empty((0, 32), dtype=torch.int8, device="cuda")
