@@ -543,13 +543,15 @@ def _call(what, dev, stream, fn, *args):
 def _new(shape, dtype, like, stream):
     """A result's memory, allocated on the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _codes(T, K, like, stream):
     """An int8 [T, K] whose rows start on 16 bytes, as the products read them."""
+    if K % 16 == 0:
+        return _new((T, K), torch.int8, like, stream)
     return _new((T, -(-K // 16) * 16), torch.int8, like, stream)[:, :K]
 
 
