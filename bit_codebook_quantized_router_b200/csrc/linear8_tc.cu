@@ -321,8 +321,12 @@ __device__ __forceinline__ void store_row16(const LinArgs& a, int align, float* 
   __syncwarp();
 }
 
-template <bool GATED, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// SPLIT > 1: a cluster of SPLIT pairs has one tile; each pair multiplies a part
+// of K and finishes a part of the columns, with the others' int32 sums of them
+// (exact, so the result's bits are those of the unsplit kernel), which they send
+// to its ring once it is done with.
+template <bool GATED, int BN, int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     wide_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ CUtensorMap tm_x,
                 const __grid_constant__ CUtensorMap tm_w) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -333,14 +337,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + kWideStages;
   uint64_t* acc_full = empty + kWideStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2], the even CTA's
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* ready = acc_empty + 2;           // SPLIT: the others' rings are done with
+  uint64_t* in_full = ready + 1;             // SPLIT: the others' sums are here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_scale = reinterpret_cast<float*>(sB + kWideStages * kTile + 512);  // [2][256] the columns' scales
   float* s_bias = s_scale + 512;                                              // [2][256] and biases
   float* s_rows = s_bias + 512;                                               // [epilogue warps][32][kWideRow]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
+  const int rank = (int)cluster_rank() & 1, part = SPLIT > 1 ? (int)cluster_rank() >> 1 : 0, lead = 2 * part;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&full[s], 1);
@@ -349,6 +355,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    if (SPLIT > 1) {
+      mbar_init(ready, SPLIT - 1);
+      mbar_init(in_full, (SPLIT - 1) * kEpiWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -367,8 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr int kBN = GATED ? BN / 2 : BN;  // output columns of a tile
   const int n_tiles = (a.N + kBN - 1) / kBN;
   const int total = m_tiles * n_tiles;
-  const int ksteps = (a.K + kBK - 1) / kBK;
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int all = (a.K + kBK - 1) / kBK, k_lo = all * part / SPLIT, ksteps = all * (part + 1) / SPLIT - k_lo;
+  const int first = blockIdx.x / (2 * SPLIT), step = gridDim.x / (2 * SPLIT);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -383,8 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int s = it % kWideStages;
           if (!(ok = mbar_wait(&empty[s], ((it / kWideStages) & 1) ^ 1, abort_flag, kWaitNs))) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kTile + BN / 2 * kBK));
-          const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
-          tma_load_2d_pair(sB + s * kTile, &tm_w, bar, ks * kBK, yb);
+          const uint32_t bar = cluster_addr(smem_u32(&full[s]), lead);
+          tma_load_2d_pair(sB + s * kTile, &tm_w, bar, (k_lo + ks) * kBK, yb);
           // in a chain the ring's first weights are asked for before the
           // kernel in front is done with the tokens (elsewhere step by step:
           // weights first costs 1 us)
@@ -392,10 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if ((int)it + 1 < min(kWideStages, ksteps)) continue;
             pdl_wait();
             for (int i = 0; i < ks; ++i)
-              tma_load_2d_pair(sA + i * kTile, &tm_x, cluster_addr(smem_u32(&full[i]), 0), i * kBK, ya);
+              tma_load_2d_pair(sA + i * kTile, &tm_x, cluster_addr(smem_u32(&full[i]), lead), (k_lo + i) * kBK, ya);
             filled = true;
           }
-          tma_load_2d_pair(sA + s * kTile, &tm_x, bar, ks * kBK, ya);
+          tma_load_2d_pair(sA + s * kTile, &tm_x, bar, (k_lo + ks) * kBK, ya);
         }
       }
       // the last MMAs' arrivals at this CTA's barriers, so that none comes after its end
@@ -421,9 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk)
             umma_s8<true>(d, da + 2 * kk, db + 2 * kk, idesc, (ks | kk) != 0);
-          umma_commit_pair(&empty[s]);
+          umma_commit_pair(&empty[s], lead);
         }
-        if (ok) umma_commit_pair(&acc_full[buf]);
+        if (ok) umma_commit_pair(&acc_full[buf], lead);
       }
       // the last tiles' arrivals from the pair's other CTA, so that none comes
       // after this one's end
@@ -456,10 +466,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lost || (lost = !mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs))) continue;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
-      constexpr int kCols = kBN / 2;  // of this warp
+      constexpr int kOwn = kBN / SPLIT, kCols = kOwn / 2;  // columns of this pair, of this warp
+      constexpr int kPlanes = GATED ? 2 : 1;
+      // [SPLIT - 1][kPlanes][kOwn / 4][128 rows][4 columns]: a warp writes and reads 512 consecutive bytes
+      const uint32_t inbox = smem_u32(sA) + (quad * 32 + lane) * 16;
+      if (SPLIT > 1) {
+        // this CTA's ring is free; once the others' are, their columns' sums go there
+        if (e < SPLIT && e != part) mbar_arrive_cluster(cluster_addr(smem_u32(ready), 2 * e + rank));
+        if ((lost = !mbar_wait_warp<true>(ready, 0, abort_flag, kWaitNs))) continue;
+#pragma unroll
+        for (int d = 1; d < SPLIT; ++d) {
+          const int to = (part + d) % SPLIT;
+          const uint32_t at = cluster_addr(inbox + (d - 1) * kPlanes * kOwn * 512, 2 * to + rank);
+#pragma unroll
+          for (int pl = 0; pl < kPlanes; ++pl)
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t w[16];
+              tmem_ld16_nowait(tb + pl * kBN + to * kOwn + half * kCols + c, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) cluster_st128(at + (pl * kOwn + half * kCols + c + j) * 512, w + j);
+            }
+        }
+        __syncwarp();
+        if (lane < SPLIT && lane != part) mbar_arrive_cluster(cluster_addr(smem_u32(in_full), 2 * lane + rank));
+        __syncwarp();
+        if ((lost = !mbar_wait_warp<true>(in_full, 0, abort_flag, kWaitNs))) continue;
+      }
       uint32_t v[2][16], u[2][16];
       auto load = [&](int i) {
-        const int c = half * kCols + i * 16;
+        const int c = part * kOwn + half * kCols + i * 16;
         tmem_ld16_nowait(tb + c, v[i & 1]);
         if (GATED) tmem_ld16_nowait(tb + kBN + c, u[i & 1]);
       };
@@ -472,9 +509,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[buf]), 0));
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[buf]), lead));
         }
-        const int c = half * kCols + i * 16;
+        if (SPLIT > 1) {
+#pragma unroll
+          for (int src = 0; src < SPLIT - 1; ++src)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const uint32_t at = inbox + (src * kPlanes * kOwn + half * kCols + i * 16 + j) * 512;
+              auto add = [](uint32_t d[4], uint4 w) { d[0] += w.x, d[1] += w.y, d[2] += w.z, d[3] += w.w; };
+              add(v[i & 1] + j, lds32x4(at));
+              if (GATED) add(u[i & 1] + j, lds32x4(at + kOwn * 512));
+            }
+        }
+        const int c = part * kOwn + half * kCols + i * 16;
         const float* sc = s_scale + buf * 256 + c;
         const float* sb = s_bias + buf * 256 + c;
         const F2 xs2 = f2(xs, xs);
@@ -600,7 +648,7 @@ int launch_mid(const LinArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, mid_kernel<GATED>, a, p, tx, tw) == cudaSuccess ? MOE_Q4_OK : MOE_Q4_ECUDA;
 }
 
-template <bool GATED, int BN>
+template <bool GATED, int BN, int SPLIT>
 int launch_wide(const LinArgs& a, cudaStream_t s) {
   constexpr int cols = GATED ? BN / 2 : BN;
   const long long tiles = (((long long)a.T + 255) / 256) * ((a.N + cols - 1) / cols);
@@ -609,11 +657,11 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
   if (!map_rows(&tx, a.x, a.K, a.T, a.ldx, 128) ||
       !map_rows(&tw, a.w, a.K, GATED ? 2ull * a.N : a.N, a.ldw, BN / 2))
     return MOE_Q4_ECUDA;
-  const auto kernel = wide_kernel<GATED, BN>;
+  const auto kernel = wide_kernel<GATED, BN, SPLIT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
     return MOE_Q4_ECUDA;
   const int pairs = sm_count() / 2;
-  const int grid = 2 * (int)(tiles < pairs ? tiles : pairs);
+  const int grid = SPLIT > 1 ? 2 * SPLIT * (int)tiles : 2 * (int)(tiles < pairs ? tiles : pairs);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -634,10 +682,22 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
   // leave SMs idle: each then writes fewer results (T = 256, N = 6144,
   // K = 2048: 12.6 us with 256 columns, 11.9 with 128, 14.8 with 64 in two
   // turns; N = K = 512: 8.0, 6.6 and 5.8).
-  const long long m = (a.T + 255) / 256, pairs = sm_count() / 2, n = GATED ? 2ll * a.N : a.N;
-  if (m * ((n + 63) / 64) <= pairs) return launch_wide<GATED, 64>(a, s);
-  if (m * ((n + 127) / 128) <= pairs) return launch_wide<GATED, 128>(a, s);
-  return launch_wide<GATED, 256>(a, s);
+  const long long m = (a.T + 255) / 256, sms = sm_count(), pairs = sms / 2, n = GATED ? 2ll * a.N : a.N;
+  const long long t128 = m * ((n + 127) / 128), t256 = m * ((n + 255) / 256);
+  // A long K is split over the pairs of a cluster where the clusters fit the
+  // card at once (32 of four CTAs, 15 of eight): the exchange of the sums costs
+  // what 10 to 20 k-steps do.  Measured at 256 tokens, us, unsplit and split:
+  // N = 2048 in tiles of 128 over two pairs, K = 2048 8.0 and 8.1, K = 2560 9.1
+  // and 8.7, K = 4096 12.9 and 10.8; N = 6144 in tiles of 256, K = 2560 11.1 and
+  // 12.0, K = 4096 14.8 and 14.0 (N = 8192 15.0 and 15.1), K = 6144 19.5 and
+  // 16.5; N = 512 over two and four pairs, K = 3584 9.5 and 9.8, K = 5120 11.3
+  // and 10.6, K = 8192 14.7 and 12.4.
+  if (a.K >= 5120 && 8 * t256 <= sms * 5 / 6) return launch_wide<GATED, 256, 4>(a, s);
+  if (a.K >= 2560 && 4 * t128 <= sms * 8 / 9) return launch_wide<GATED, 128, 2>(a, s);
+  if (a.K >= 4096 && 4 * t256 <= sms * 8 / 9) return launch_wide<GATED, 256, 2>(a, s);
+  if (m * ((n + 63) / 64) <= pairs) return launch_wide<GATED, 64, 1>(a, s);
+  if (m * ((n + 127) / 128) <= pairs) return launch_wide<GATED, 128, 1>(a, s);
+  return launch_wide<GATED, 256, 1>(a, s);
 }
 
 }  // namespace

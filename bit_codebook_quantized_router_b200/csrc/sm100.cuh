@@ -334,6 +334,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint4 lds32x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---- clusters and CTA pairs -----------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -359,6 +365,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 
 __device__ __forceinline__ void cluster_st32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_st128(uint32_t addr, const uint32_t v[4]) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -401,12 +412,12 @@ __device__ __forceinline__ void umma_s8(uint32_t tmem_d, uint64_t adesc, uint64_
         : "memory");
 }
 
-// Arrive on this barrier of both CTAs of the pair once every tcgen05 op
-// issued so far by this thread is done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrive on this barrier of both CTAs of the pair (the cluster's ranks lead and
+// lead + 1) once every tcgen05 op issued so far by this thread is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, int lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+      ::"r"(smem_u32(bar)), "h"((uint16_t)(3 << lead)) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {

@@ -237,6 +237,39 @@ def test_linear(T, N, K, dtype, bias):
     check_linear(got, x, xs, w, ws, b)
 
 
+@pytest.mark.parametrize("T,N,K", [(129, 100, 2560), (129, 100, 2559), (256, 515, 2700), (200, 77, 5120),
+                                   (257, 300, 5121), (300, 1800, 5200),
+                                   (256, 2049, 5120), (256, 4000, 2561), (256, 4200, 4096), (400, 2100, 4500), (256, 8192, 4097),
+                                   (256, 8200, 4097), (1000, 1000, 2600), (900, 100, 131071)])
+@pytest.mark.parametrize("dtype,bias", [(BF, False), (F, True)])
+def test_linear_long_rows_of_many_tokens(T, N, K, dtype, bias):
+    # K over a cluster's pairs, and both sides of the limits: exact sums against
+    # a split of the same product into calls of few tokens, and the plain form
+    x, xs = int8_rows(T, K, K, extreme=True)
+    w, ws = int8_rows(N, K, K + 7, extreme=True)
+    b = torch.randn(N, generator=gen(N)).cuda() if bias else None
+    xg, xsg, wg, wsg = on_gpu(x), xs.cuda(), on_gpu(w), ws.cuda()
+    out, status = Guarded((T, N), dtype), torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = q4.linear_i8(xg, xsg, wg, wsg, bias=b, out=out.view, status=status)
+    out.check("out")
+    assert status.item() == 0
+    for lo in (0, T // 2, T - 16):
+        few = q4.linear_i8(xg[lo:lo + 16], xsg[lo:lo + 16], wg, wsg, bias=b, dtype=dtype)
+        assert torch.equal(few, got[lo:lo + 16])
+    some = slice(T - 5, T)
+    check_linear(got[some], x[some], xs[some], w, ws, None if b is None else b.cpu())
+
+
+@pytest.mark.parametrize("T,H,I", [(129, 2560, 65), (256, 5200, 130), (256, 4100, 2050), (256, 5120, 1030), (513, 2600, 400)])
+def test_mlp_long_rows_of_many_tokens(T, H, I):
+    m = mlp_weights(H, I, H + I)
+    q, s = q4.quant_rows(rows(T, H, T, spread=False).cuda())
+    got = q4.mlp_i8(m, q, s, dtype=F)
+    for lo in (0, T // 2, T - 9):
+        assert torch.equal(q4.mlp_i8(m, q[lo:lo + 9], s[lo:lo + 9], dtype=F), got[lo:lo + 9])
+    check_mlp(got[-5:], m, q[-5:].cpu(), s[-5:].cpu())
+
+
 @pytest.mark.parametrize("T", [1, 20, 130, 600])
 @pytest.mark.parametrize("ldx,ldw,ldo", [(64, 80, 101), (128, 64, 104), (80, 192, 112)])
 def test_linear_strides(T, ldx, ldw, ldo):
