@@ -38,6 +38,19 @@ __device__ __noinline__ uint4 load_some(const int8_t* p, int n) {
   return n & 8 ? make_uint4(d.x, d.y, e, f) : make_uint4(e, f, 0, 0);
 }
 
+// 16 bytes of a weight row: read once, so not kept in L1, and through the
+// coherent path.  The kernel in front may write the weights while this one is
+// already resident (outside a chain they are read after its wait), and the
+// read-only path is for what does not change in a kernel's whole life.
+__device__ __forceinline__ uint4 load_weight(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // The 16 bytes of a row at k, zeros past its end K (nothing is read there).
 __device__ __forceinline__ uint4 load_row16(const int8_t* row, int k, int K) {
   if (k + 16 <= K) return *reinterpret_cast<const uint4*>(row + k);
@@ -48,7 +61,7 @@ __device__ __forceinline__ uint4 load_row16(const int8_t* row, int k, int K) {
 // hold its end is taken as it is (it meets the tokens' zeros), but nothing is
 // read behind the last row.
 __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, bool last) {
-  return k < K && !last ? ldg_stream(row + k) : load_row16(row, k, K);
+  return k < K && !last ? load_weight(row + k) : load_row16(row, k, K);
 }
 
 // Few tokens: 16 weight rows a CTA (8 gate and 8 up rows when GATED), 8 NT
@@ -77,7 +90,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
   auto load_x = [&](int n, int k, bool whole) {
     const int t = 8 * n + g;
     if (t >= a.T) return make_uint4(0, 0, 0, 0);
-    // (no read-only path: in a chain the rows are written while this kernel runs)
+    // (no read-only path: the rows may be written while this kernel is resident)
     if (whole) return *reinterpret_cast<const uint4*>(a.x + t * a.ldx + k);
     return load_row16(a.x + t * a.ldx, k, a.K);
   };
@@ -92,8 +105,8 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = (sg + u * warps) * 128 + h * 64 + 16 * t4;
-        va[u][h] = ldg_stream(wa + k);
-        vb[u][h] = ldg_stream(wb + k);
+        va[u][h] = load_weight(wa + k);
+        vb[u][h] = load_weight(wb + k);
       }
   };
   int sg = warp;
@@ -125,7 +138,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = sg * 128 + h * 64 + 16 * t4;
-      const uint4 p = ldg_stream(wa + k), q = ldg_stream(wb + k);
+      const uint4 p = load_weight(wa + k), q = load_weight(wb + k);
 #pragma unroll
       for (int n = 0; n < NT; ++n) product(n, p, q, load_x(n, k, true));
     }
