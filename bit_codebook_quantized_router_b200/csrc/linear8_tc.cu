@@ -414,6 +414,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
+      pdl_wait();  // (so that the waits' limits do not count the kernel in front, however long it runs)
       const uint32_t idesc = umma_idesc_s8(256, BN);
       uint32_t it = 0, use = 0;
       bool ok = true;

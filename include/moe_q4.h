@@ -565,6 +565,12 @@ MOE_Q4_API int moe_q4_forward_gated_i8(const moe_q4_layer* layer, const moe_q4_m
  * ------------------------------------------------------------------------- */
 MOE_Q4_API int moe_q4_selftest_wait(int32_t* status, unsigned limit_us, void* stream);
 
+/* moe_q4_selftest_hold -- test support: one CTA that lets the stream's next
+ * kernel start at once (programmatic dependent launch) and then runs for `us`
+ * microseconds (1 .. 3,000,000) by itself.  The time that a kernel behind it
+ * sits out does not count against that kernel's own bounded waits. */
+MOE_Q4_API int moe_q4_selftest_hold(unsigned us, void* stream);
+
 /* Synchronise `stream` and return the int32 at device address `status`
  * (as written by moe_q4_pack), or MOE_Q4_ECUDA. */
 MOE_Q4_API int moe_q4_read_status(const int32_t* status, void* stream);

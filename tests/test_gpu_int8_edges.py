@@ -1,9 +1,12 @@
 """The 8-bit integer operators at the edges of what their callers may do."""
+import ctypes
+
 import pytest
 import torch
 
 import bit_codebook_quantized_router_b200 as q4
-from tests.test_gpu_int8 import F, rows
+from bit_codebook_quantized_router_b200 import _lib
+from tests.test_gpu_int8 import F, mlp_weights, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +44,25 @@ def test_weights_written_by_the_kernel_in_front(T, N, K):
     for got in (eager, captured):
         for i, y in enumerate(got):
             assert torch.equal(y, want[i % 3]), i
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 400, 512), (200, 400, 2600), (200, 100, 5200), (64, 512, 2048), (8, 512, 2048)])
+def test_limits_do_not_count_the_kernel_in_front(T, N, K):
+    # the kernel in front lets the product start and then runs for longer than
+    # any of the product's waits may take
+    x, xs = q4.quant_rows(rows(T, K, 1, spread=False).cuda())
+    w, ws = q4.quant_rows(rows(N, K, 2, spread=False).cuda())
+    m = mlp_weights(K, 128, 3)
+    want, want_mlp = q4.linear_i8(x, xs, w, ws, dtype=F), q4.mlp_i8(m, x, xs, dtype=F)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, got_mlp = torch.zeros_like(want), torch.zeros_like(want_mlp)
+    ws_mlp = q4.alloc_workspace(q4.mlp_i8_workspace(m, T))
+    torch.cuda.synchronize()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert q4.lib().moe_q4_selftest_hold(2300000, stream) == _lib.OK  # the limit is 2 s
+    q4.linear_i8(x, xs, w, ws, out=got, status=status)
+    assert q4.lib().moe_q4_selftest_hold(2300000, stream) == _lib.OK
+    q4.mlp_i8(m, x, xs, out=got_mlp, ws=ws_mlp, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    assert torch.equal(got, want) and torch.equal(got_mlp, want_mlp)
