@@ -24,6 +24,10 @@ struct LinArgs {
   int T, N, K;
   int out_f32;
   int chained;           // behind a kernel of the same call: the weights may be read before it is done
+#ifdef MOE_Q4_DEBUG
+  uint64_t limit_ns;     // test support, moe_q4_debug_withhold
+  int withheld, late;
+#endif
 };
 
 // The one place that turns a sum into a value: the same bits in every kernel.

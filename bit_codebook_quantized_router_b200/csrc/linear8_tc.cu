@@ -56,6 +56,22 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// The waits' limit, and in the debug build what a test withholds to make one
+// run out (moe_q4_debug_withhold).
+#ifdef MOE_Q4_DEBUG
+__device__ __forceinline__ uint64_t wait_ns(const LinArgs& a) { return a.limit_ns; }
+__device__ __forceinline__ bool withheld(const LinArgs& a, int block) { return block == a.withheld && !a.late; }
+__device__ __forceinline__ void send_late(const LinArgs& a, int block) {
+  if (block != a.withheld || !a.late) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 4 * a.limit_ns) __nanosleep(1000);
+}
+#else
+__device__ __forceinline__ constexpr uint64_t wait_ns(const LinArgs&) { return kWaitNs; }
+__device__ __forceinline__ constexpr bool withheld(const LinArgs&, int) { return false; }
+__device__ __forceinline__ void send_late(const LinArgs&, int) {}
+#endif
+
 // On an abandoned wait: record it and let the copies in flight land before
 // the shared memory goes away.
 __device__ __forceinline__ void give_up(int32_t* status, uint64_t* full, int stages) {
@@ -105,7 +121,10 @@ __global__ void __launch_bounds__(kThreads)
     tma_load_2d(sA + s * kTile, &tm_w, &full[s], ks * kBK, n0);
     if (GATED) tma_load_2d(sA + s * kTile + kTile / 2, &tm_w, &full[s], ks * kBK, a.N + n0);
   };
-  auto load_x = [&](int ks, int s) { tma_load_2d(sB + s * b_tile, &tm_x, &full[s], ks * kBK, 0); };
+  const int block = blockIdx.x * splits + rank;
+  auto load_x = [&](int ks, int s) {
+    if (ks != k_lo || !withheld(a, block)) tma_load_2d(sB + s * b_tile, &tm_x, &full[s], ks * kBK, 0);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -140,7 +159,6 @@ __global__ void __launch_bounds__(kThreads)
   const int n = n0 + (et & (kRows - 1));
   float wscale = 0.0f, uscale = 0.0f, bias = 0.0f;
   pdl_wait();  // (before these loads: it waits for them)
-  pdl_trigger();
   if (et >= 0 && n < a.N) {
     wscale = a.ws[n];
     if (GATED) uscale = a.ws[a.N + n];
@@ -148,6 +166,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   tc_fence_before();
   __syncthreads();
+  pdl_trigger();  // (once this CTA has its tensor memory: the next kernel's CTAs may ask for all that is left)
   cluster_arrive_relaxed();  // this CTA's barriers are ready (waited for before anything is sent)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -157,7 +176,7 @@ __global__ void __launch_bounds__(kThreads)
       int it = S;
       for (int ks = k_lo + S; ks < k_hi; ++ks, ++it) {
         const int s = it % S;
-        if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort_flag, kWaitNs)) break;
+        if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort_flag, wait_ns(a))) break;
         load_w(ks, s);
         load_x(ks, s);
       }
@@ -168,7 +187,7 @@ __global__ void __launch_bounds__(kThreads)
       int it = 0;
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
         const int s = it % S;
-        if (!mbar_wait(&full[s], (it / S) & 1, abort_flag, kWaitNs)) break;
+        if (!mbar_wait(&full[s], (it / S) & 1, abort_flag, wait_ns(a))) break;
         tc_fence_after();
         const uint64_t da = umma_desc_sw128(smem_u32(sA + s * kTile));
         const uint64_t db = umma_desc_sw128(smem_u32(sB + s * b_tile));
@@ -178,7 +197,7 @@ __global__ void __launch_bounds__(kThreads)
         umma_commit(&empty[s]);
       }
       umma_commit(acc_full);
-      mbar_wait(acc_full, 0, abort_flag, kWaitNs);
+      mbar_wait(acc_full, 0, abort_flag, wait_ns(a));
     }
   } else if (et < c_n) {
     s_xs[et] = a.xs[c_lo + et];
@@ -189,7 +208,12 @@ __global__ void __launch_bounds__(kThreads)
   __syncwarp();
   cluster_wait();
   tc_fence_after();
-  if (warp >= kEpiWarp0) {
+  // The second barrier of the cluster: no CTA ends, and its shared memory with
+  // it, before every other has sent, whatever wait was given up.
+  if (warp < kEpiWarp0) {
+    cluster_arrive_relaxed();
+  } else {
+    send_late(a, block);
     // send: columns [own * r, own * (r + 1)) to CTA r as [src][column][128
     // rows], a warp 128 consecutive bytes at a time (16 bytes a lane at a row's
     // pitch measured slower, 17.1 against 14.6 us at 64 tokens and 6144 x 6144,
@@ -213,12 +237,13 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
     if (lane < splits) mbar_arrive_cluster(cluster_addr(smem_u32(in_full), lane));
     __syncwarp();
+    cluster_arrive_relaxed();  // (the arrivals in front waited for what was sent)
     tc_fence_before();
 
     // finish this CTA's columns, four at a time, once all their sums are here
-    // (a CTA that gave a wait up sends too, after give_up; so this one is longer
-    // than that takes and has a flag of its own: no CTA ends while another sends)
-    if (!mbar_wait_warp<true>(in_full, 0, in_abort, 3 * kWaitNs)) *abort_flag = 1;
+    // (a CTA that gave a wait up sends what it has all the same, so this wait is
+    // longer than those, and has a flag of its own)
+    if (!mbar_wait_warp<true>(in_full, 0, in_abort, 3 * wait_ns(a))) *abort_flag = 1;
     if (n < a.N) {
       constexpr int kStep = 32 * kEpiWarps / kRows;
       const uint32_t box = inbox + (et & (kRows - 1)) * 4;
@@ -248,6 +273,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) record_error(a.status, MOE_Q4_ETIMEOUT);
+  cluster_wait();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -384,6 +410,9 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true, filled = !a.chained;
+      auto load_x = [&](int s, uint32_t bar, int ks, int y, bool first) {
+        if (!first || !withheld(a, blockIdx.x)) tma_load_2d_pair(sA + s * kTile, &tm_x, bar, (k_lo + ks) * kBK, y);
+      };
       if (!a.chained) pdl_wait();
       for (int tile = first; tile < total && ok; tile += step) {
         const int m = tile % m_tiles, n = tile / m_tiles;
@@ -391,7 +420,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
         const int yb = GATED ? rank * a.N + n * kBN : n * BN + rank * (BN / 2);
         for (int ks = 0; ks < ksteps; ++ks, ++it) {
           const int s = it % kWideStages;
-          if (!(ok = mbar_wait(&empty[s], ((it / kWideStages) & 1) ^ 1, abort_flag, kWaitNs))) break;
+          if (!(ok = mbar_wait(&empty[s], ((it / kWideStages) & 1) ^ 1, abort_flag, wait_ns(a)))) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kTile + BN / 2 * kBK));
           const uint32_t bar = cluster_addr(smem_u32(&full[s]), lead);
           tma_load_2d_pair(sB + s * kTile, &tm_w, bar, (k_lo + ks) * kBK, yb);
@@ -401,16 +430,15 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
           if (!filled) {
             if ((int)it + 1 < min(kWideStages, ksteps)) continue;
             pdl_wait();
-            for (int i = 0; i < ks; ++i)
-              tma_load_2d_pair(sA + i * kTile, &tm_x, cluster_addr(smem_u32(&full[i]), lead), (k_lo + i) * kBK, ya);
+            for (int i = 0; i < ks; ++i) load_x(i, cluster_addr(smem_u32(&full[i]), lead), i, ya, i == 0);
             filled = true;
           }
-          tma_load_2d_pair(sA + s * kTile, &tm_x, bar, (k_lo + ks) * kBK, ya);
+          load_x(s, bar, ks, ya, it == 0);
         }
       }
       // the last MMAs' arrivals at this CTA's barriers, so that none comes after its end
       for (int j = 0; j < kWideStages && ok; ++j, ++it)
-        ok = mbar_wait(&empty[it % kWideStages], ((it / kWideStages) & 1) ^ 1, abort_flag, kWaitNs);
+        ok = mbar_wait(&empty[it % kWideStages], ((it / kWideStages) & 1) ^ 1, abort_flag, wait_ns(a));
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -420,12 +448,12 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = first; tile < total && ok; tile += step, ++use) {
         const int buf = use & 1;
-        if (!(ok = mbar_wait(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, kWaitNs))) break;
+        if (!(ok = mbar_wait(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, wait_ns(a)))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
         for (int ks = 0; ks < ksteps; ++ks, ++it) {
           const int s = it % kWideStages;
-          if (!(ok = mbar_wait(&full[s], (it / kWideStages) & 1, abort_flag, kWaitNs))) break;
+          if (!(ok = mbar_wait(&full[s], (it / kWideStages) & 1, abort_flag, wait_ns(a)))) break;
           tc_fence_after();
           const uint64_t da = umma_desc_sw128(smem_u32(sA + s * kTile));
           const uint64_t db = umma_desc_sw128(smem_u32(sB + s * kTile));
@@ -439,7 +467,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
       // the last tiles' arrivals from the pair's other CTA, so that none comes
       // after this one's end
       for (uint32_t u = use > 2 ? use - 2 : 0; u < use && ok; ++u)
-        ok = mbar_wait(&acc_empty[u & 1], (u >> 1) & 1, abort_flag, kWaitNs);
+        ok = mbar_wait(&acc_empty[u & 1], (u >> 1) & 1, abort_flag, wait_ns(a));
     }
   } else {
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2, e = threadIdx.x - 32 * kEpiWarp0;
@@ -464,7 +492,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
       const float xs = t < a.T ? a.xs[t] : 0.0f;
       named_bar(1, 32 * kEpiWarps);
       // (a warp whose wait was given up still meets the others at the barrier)
-      if (lost || (lost = !mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, kWaitNs))) continue;
+      if (lost || (lost = !mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, wait_ns(a)))) continue;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
       constexpr int kOwn = kBN / SPLIT, kCols = kOwn / 2;  // columns of this pair, of this warp
@@ -474,7 +502,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
       if (SPLIT > 1) {
         // this CTA's ring is free; once the others' are, their columns' sums go there
         if (e < SPLIT && e != part) mbar_arrive_cluster(cluster_addr(smem_u32(ready), 2 * e + rank));
-        if ((lost = !mbar_wait_warp<true>(ready, 0, abort_flag, kWaitNs))) continue;
+        if ((lost = !mbar_wait_warp<true>(ready, 0, abort_flag, wait_ns(a)))) continue;
 #pragma unroll
         for (int d = 1; d < SPLIT; ++d) {
           const int to = (part + d) % SPLIT;
@@ -493,7 +521,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane < SPLIT && lane != part) mbar_arrive_cluster(cluster_addr(smem_u32(in_full), 2 * lane + rank));
         __syncwarp();
-        if ((lost = !mbar_wait_warp<true>(in_full, 0, abort_flag, kWaitNs))) continue;
+        if ((lost = !mbar_wait_warp<true>(in_full, 0, abort_flag, wait_ns(a)))) continue;
       }
       uint32_t v[2][16], u[2][16];
       auto load = [&](int i) {
@@ -705,10 +733,28 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
 
 }  // namespace q4
 
+#ifdef MOE_Q4_DEBUG
+static uint64_t debug_limit_ns = q4::kWaitNs;
+static int debug_block = -1, debug_late = 0;
+
+extern "C" int moe_q4_debug_withhold(int block, int late, unsigned limit_us) {
+  if (block < -1 || limit_us == 0 || limit_us > 2000000u) return MOE_Q4_EINVAL;
+  debug_block = block, debug_late = late, debug_limit_ns = (uint64_t)limit_us * 1000ull;
+  return MOE_Q4_OK;
+}
+
+static q4::LinArgs with_debug(q4::LinArgs a) {
+  a.limit_ns = debug_limit_ns, a.withheld = debug_block, a.late = debug_late;
+  return a;
+}
+#else
+static const q4::LinArgs& with_debug(const q4::LinArgs& a) { return a; }
+#endif
+
 int q4_launch_linear_mid(const q4::LinArgs& a, bool gated, cudaStream_t s) {
-  return gated ? q4::launch_mid<true>(a, s) : q4::launch_mid<false>(a, s);
+  return gated ? q4::launch_mid<true>(with_debug(a), s) : q4::launch_mid<false>(with_debug(a), s);
 }
 
 int q4_launch_linear_wide(const q4::LinArgs& a, bool gated, cudaStream_t s) {
-  return gated ? q4::launch_wide<true>(a, s) : q4::launch_wide<false>(a, s);
+  return gated ? q4::launch_wide<true>(with_debug(a), s) : q4::launch_wide<false>(with_debug(a), s);
 }
