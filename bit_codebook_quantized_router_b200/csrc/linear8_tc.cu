@@ -737,7 +737,12 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
 static uint64_t debug_limit_ns = q4::kWaitNs;
 static int debug_block = -1, debug_late = 0;
 
-extern "C" int moe_q4_debug_withhold(int block, int late, unsigned limit_us) {
+// Test support, this build only: from now on the products of this file limit
+// their device waits to limit_us (1 .. 2,000,000; the release build's is the
+// last), and block `block` of each launch (-1: none) never asks for its first
+// tokens or, with `late` (to 128 tokens), sends its partial sums only after four
+// limits, so that waits run out.  Not for calls from several threads.
+extern "C" MOE_Q4_API int moe_q4_debug_withhold(int block, int late, unsigned limit_us) {
   if (block < -1 || limit_us == 0 || limit_us > 2000000u) return MOE_Q4_EINVAL;
   debug_block = block, debug_late = late, debug_limit_ns = (uint64_t)limit_us * 1000ull;
   return MOE_Q4_OK;

@@ -571,16 +571,6 @@ MOE_Q4_API int moe_q4_selftest_wait(int32_t* status, unsigned limit_us, void* st
  * sits out does not count against that kernel's own bounded waits. */
 MOE_Q4_API int moe_q4_selftest_hold(unsigned us, void* stream);
 
-#ifdef MOE_Q4_DEBUG
-/* moe_q4_debug_withhold -- test support, debug build only: from now on the int8
- * products of more than a few tokens limit their device waits to limit_us
- * (1 .. 2,000,000; 2,000,000 is the release build's), and block `block` of each
- * launch (-1: none) never asks for its first tokens or, with `late` != 0, sends
- * its partial sums to its cluster only after four limits (up to 128 tokens), so
- * that waits run out.  Not for calls from several threads. */
-MOE_Q4_API int moe_q4_debug_withhold(int block, int late, unsigned limit_us);
-#endif
-
 /* Synchronise `stream` and return the int32 at device address `status`
  * (as written by moe_q4_pack), or MOE_Q4_ECUDA. */
 MOE_Q4_API int moe_q4_read_status(const int32_t* status, void* stream);
