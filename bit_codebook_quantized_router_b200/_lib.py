@@ -101,6 +101,7 @@ def lib():
         L.moe_q4_add_norm.argtypes = [vp, ci, ll, vp, ci, ll, vp, ll, vp, ci, ctypes.c_float, ci, ci, vp, ll, vp, ll,
                                       vp, vp]
         L.moe_q4_linear_i8.argtypes = [vp, ll, vp, vp, ll, vp, vp, ci, ci, ci, vp, ci, ll, vp, vp]
+        L.moe_q4_i8_status.argtypes = [vp]
         L.moe_q4_mlp_i8_workspace.argtypes = [mlp, ci]
         L.moe_q4_mlp_i8.argtypes = [mlp, vp, ll, vp, ci, vp, ci, ll, vp, vp, sz, vp]
         layer = ctypes.POINTER(_LayerStruct)
@@ -111,7 +112,7 @@ def lib():
                                               vp]
         for f in (L.moe_q4_mlp_i8_workspace, L.moe_q4_forward_ex_i8_workspace, L.moe_q4_forward_gated_i8_workspace):
             f.restype = sz
-        for f in (L.moe_q4_quant_rows, L.moe_q4_add_norm, L.moe_q4_linear_i8, L.moe_q4_mlp_i8,
+        for f in (L.moe_q4_quant_rows, L.moe_q4_add_norm, L.moe_q4_linear_i8, L.moe_q4_mlp_i8, L.moe_q4_i8_status,
                   L.moe_q4_forward_ex_i8, L.moe_q4_forward_gated_i8):
             f.restype = ci
         for f in (L.moe_q4_pack, L.moe_q4_dequant, L.moe_q4_forward, L.moe_q4_forward_host,
@@ -615,7 +616,8 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     with scales w_scale [N], sums exact in int32: out [T, N] in bf16 or fp32
     (dtype, or out's), plus an fp32 bias [N].  The rows of x and w start on
     16-byte boundaries (quant_rows makes them so).  status: an int32 CUDA
-    tensor [1] that receives the code of a device wait that gave up."""
+    tensor [1] that receives the code of a device wait that gave up; without
+    one i8_status() tells."""
     dev, T, K, ldx = _first(x, "x", _INT8)
     N = w.shape[0]
     if out is None:
@@ -626,6 +628,14 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
           _ROW_TYPE.get(out.dtype, -1), _rows(out, "out", dev, T, N, _ROW_TYPE),
           None if status is None else _vector(status, "status", dev, 1, _INT32))
     return out
+
+
+def i8_status(device=None, stream=None) -> int:
+    """Waits for the stream; the code of a device wait that gave up in a
+    linear_i8 or mlp_i8 call without a status tensor on the device (0: none),
+    which is cleared once it was returned."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(lib().moe_q4_i8_status(_stream(stream)))
 
 
 class MlpI8:

@@ -72,10 +72,17 @@ __device__ __forceinline__ constexpr bool withheld(const LinArgs&, int) { return
 __device__ __forceinline__ void send_late(const LinArgs&, int) {}
 #endif
 
+// The status word of calls that were given none.
+__device__ int32_t common_status;
+
+__device__ __forceinline__ void record_timeout(const LinArgs& a) {
+  record_error(a.status ? a.status : &common_status, MOE_Q4_ETIMEOUT);
+}
+
 // On an abandoned wait: record it and let the copies in flight land before
 // the shared memory goes away.
-__device__ __forceinline__ void give_up(int32_t* status, uint64_t* full, int stages) {
-  record_error(status, MOE_Q4_ETIMEOUT);
+__device__ __forceinline__ void give_up(const LinArgs& a, uint64_t* full, int stages) {
+  record_timeout(a);
   for (int s = 0; s < stages; ++s)
     for (uint32_t par = 0; par < 2; ++par) {
       volatile int quick = 0;
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   // every MMA is done, or a wait was given up
-  if (threadIdx.x == 0 && *abort_flag) give_up(a.status, full, S);
+  if (threadIdx.x == 0 && *abort_flag) give_up(a, full, S);
   __syncwarp();
   cluster_wait();
   tc_fence_after();
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) record_error(a.status, MOE_Q4_ETIMEOUT);
+  if (threadIdx.x == 0 && *abort_flag) record_timeout(a);
   cluster_wait();
   if (warp == 1) {
     __syncwarp();
@@ -583,7 +590,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) give_up(a.status, full, kWideStages);
+  if (threadIdx.x == 0 && *abort_flag) give_up(a, full, kWideStages);
   __syncthreads();
   cluster_arrive_relaxed();  // (a release would wait for the results' stores)
   cluster_wait();
@@ -732,6 +739,15 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
 }  // namespace
 
 }  // namespace q4
+
+extern "C" int moe_q4_i8_status(void* stream) {
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, q4::common_status) != cudaSuccess) return MOE_Q4_ECUDA;
+  const int rc = moe_q4_read_status(static_cast<const int32_t*>(word), stream);
+  if (rc == MOE_Q4_ETIMEOUT && cudaMemsetAsync(word, 0, sizeof(int32_t), (cudaStream_t)stream) != cudaSuccess)
+    return MOE_Q4_ECUDA;
+  return rc;
+}
 
 #ifdef MOE_Q4_DEBUG
 static uint64_t debug_limit_ns = q4::kWaitNs;

@@ -492,9 +492,10 @@ MOE_Q4_API int moe_q4_add_norm(const void* x, int x_type, long long ldx, const v
  *   T >= 0; N >= 1; 1 <= K <= 131071 (MOE_Q4_ENOTSUP above: int32 sums);
  *   out      device, bf16 or fp32 (out_type) [T][ldo] (out), aligned to its
  *            elements;
- *   status   optional device int32 (in/out), NULL to skip: left unchanged,
- *            or MOE_Q4_ETIMEOUT where it was MOE_Q4_OK if a bounded device
- *            wait gave up (out is then unspecified; moe_q4_read_status).
+ *   status   optional device int32 (in/out): left unchanged, or
+ *            MOE_Q4_ETIMEOUT where it was MOE_Q4_OK if a bounded device wait
+ *            gave up (out is then unspecified; moe_q4_read_status).  NULL: the
+ *            device's common word (moe_q4_i8_status).
  * T, N <= 2^30 (MOE_Q4_ENOTSUP above).  No workspace. */
 MOE_Q4_API int moe_q4_linear_i8(const int8_t* x, long long ldx, const float* x_scale, const int8_t* w, long long ldw,
                                 const float* w_scale, const float* bias, int T, int N, int K, void* out,
@@ -528,6 +529,13 @@ MOE_Q4_API size_t moe_q4_mlp_i8_workspace(const moe_q4_mlp* mlp, int T);
 MOE_Q4_API int moe_q4_mlp_i8(const moe_q4_mlp* mlp, const int8_t* x, long long ldx, const float* x_scale, int T,
                              void* out, int out_type, long long ldo, int32_t* status, void* ws, size_t ws_bytes,
                              void* stream);
+
+/* moe_q4_i8_status -- the common status word of moe_q4_linear_i8 and
+ * moe_q4_mlp_i8 calls that were given none, on the current device: waits for
+ * `stream` and returns MOE_Q4_OK, or MOE_Q4_ETIMEOUT if a wait of any such call
+ * has given up since the last time it was returned (returning it clears it), or
+ * MOE_Q4_ECUDA.  A call's own status word tells which call it was. */
+MOE_Q4_API int moe_q4_i8_status(void* stream);
 
 /* moe_q4_forward_ex / moe_q4_forward_gated with the shared expert as an int8
  * MLP (shared->H == layer->H): its output is added after the k routed slots in

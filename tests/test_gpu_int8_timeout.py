@@ -25,6 +25,7 @@ def L():
         getattr(lib, name).restype = ctypes.c_int
     lib.moe_q4_debug_withhold.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_uint]
     lib.moe_q4_debug_withhold.restype = ctypes.c_int
+    lib.moe_q4_i8_status.argtypes, lib.moe_q4_i8_status.restype = [ctypes.c_void_p], ctypes.c_int
     return lib
 
 
@@ -44,7 +45,7 @@ def stream():
 def linear(L, x, xs, w, ws, out, status):
     T, K = x.shape
     assert L.moe_q4_linear_i8(x.data_ptr(), x.stride(0), xs.data_ptr(), w.data_ptr(), w.stride(0), ws.data_ptr(), None, T,
-                              w.shape[0], K, out.data_ptr(), 1, out.stride(0), status.data_ptr(), stream()) == _lib.OK
+                              w.shape[0], K, out.data_ptr(), 1, out.stride(0), _lib._ptr(status), stream()) == _lib.OK
     torch.cuda.synchronize()
 
 
@@ -100,3 +101,25 @@ def test_mlp_whose_products_give_up(L, withhold, T, H, I):
         out.check("out")
         work.check("workspace")
     assert torch.equal(out.view, want)
+
+
+@pytest.mark.parametrize("T", [64, 300])
+def test_calls_without_a_status_word(L, withhold, T):
+    x, xs = q4.quant_rows(rows(T, 2176, 7, spread=False).cuda())
+    w, ws = q4.quant_rows(rows(200, 2176, 8, spread=False).cuda())
+    out = torch.empty((T, 200), device="cuda")
+    assert L.moe_q4_i8_status(stream()) == _lib.OK
+    withhold(0)
+    linear(L, x, xs, w, ws, out, None)
+    withhold(-1)
+    linear(L, x, xs, w, ws, out, None)
+    # a right call behind it does not hide it; returned once
+    assert L.moe_q4_i8_status(stream()) == _lib.ETIMEOUT
+    assert L.moe_q4_i8_status(stream()) == _lib.OK
+    # a call with a word of its own reports there alone
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    withhold(0)
+    linear(L, x, xs, w, ws, out, status)
+    assert status.item() == _lib.ETIMEOUT and L.moe_q4_i8_status(stream()) == _lib.OK
+    assert torch.equal(q4.linear_i8(x, xs, w, ws, dtype=F), q4.linear_i8(x, xs, w, ws, out=out))
+    assert q4.i8_status() == _lib.OK and q4.i8_status(device=0, stream=torch.cuda.Stream()) == _lib.OK
