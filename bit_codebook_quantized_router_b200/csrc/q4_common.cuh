@@ -158,10 +158,12 @@ __device__ __forceinline__ uint32_t ldg_u8(const uint8_t* p) {
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // The same with the hardware approximations (__expf, and __fdividef, which
-// returns 0 once 1 + e^-g overflows, as the exact form does in the limit):
-// a few ulp of fp32, far below the bf16 rounding of h that follows.
+// returns 0 once 1 + e^-g is past 2^126, where the exact form is below 1e-35 g):
+// a few ulp of fp32, and about |g| more for g far below 0, well under the bf16
+// rounding of h that follows.  silu(g) comes before u: with g u first, finite g
+// and u whose product is out of range gave infinity times 0.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) {
-  return g * u * __fdividef(1.0f, 1.0f + __expf(-g));
+  return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u;
 }
 
 constexpr int kMaxLogitsPerLane = kMaxExperts / 32;

@@ -1,0 +1,51 @@
+"""The SwiGLU at the ends of fp32's range: silu(g) u is 0 for g far below 0,
+however large u is."""
+import pytest
+import torch
+
+import bit_codebook_quantized_router_b200 as q4
+from bit_codebook_quantized_router_b200 import inputs
+from tests.test_gpu_int8 import BF, F, check_mlp, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_routed_experts(T):
+    # g = -256 and u = 2^124 or so: silu(g) u is 0 in fp32, g u is out of range
+    sh = inputs.TINY
+    tables, tid = inputs.layer_tables(inputs.WORKLOADS["tiny"])
+    gate = torch.full((sh.E, sh.I, sh.H), -1.0, dtype=BF, device="cuda")
+    up = torch.full((sh.E, sh.I, sh.H), 2.0 ** 116, dtype=BF, device="cuda")
+    down = torch.ones((sh.E, sh.H, sh.I), dtype=BF, device="cuda")
+    layer = q4.Layer(*q4.pack(gate, tables, tid), *q4.pack(up, tables, tid), *q4.pack(down, tables, tid), tables, tid)
+    x = torch.ones((T, sh.H), dtype=BF, device="cuda")
+    logits = torch.randn((T, sh.E), generator=gen(T)).cuda()
+    out32 = torch.empty((T, sh.H), device="cuda")
+    out = q4.forward(layer, x, logits, 2, out_f32=out32)
+    assert not out32.any() and not out.any()  # (a NaN counts as not zero)
+
+
+def extreme_mlp(H, I, g, u):
+    """Weights, and the codes of one row, that make channel 3's gate g and up u, both exact, beside normal channels."""
+    q = torch.randint(-127, 128, (2 * I, H), generator=gen(H), dtype=torch.int8)
+    s = torch.rand(2 * I, generator=gen(I)) * 1e-5
+    for row, v in ((3, g), (I + 3, u)):
+        q[row] = 0
+        q[row, :2] = 64 if v > 0 else -64  # sum 2^13 with the codes of x below
+        s[row] = abs(v) / 2.0 ** 13
+    x = torch.randint(-127, 128, (1, H), generator=gen(7), dtype=torch.int8)
+    x[0, :2] = 64
+    down, ds = torch.randint(-127, 128, (H, I), generator=gen(8), dtype=torch.int8), torch.rand(H, generator=gen(9)) * 1e-3
+    pad = lambda t: torch.nn.functional.pad(t, (0, -t.shape[1] % 16)).cuda()[:, :t.shape[1]]  # noqa: E731
+    return q4.MlpI8(pad(q), s.cuda(), pad(down), ds.cuda()), pad(x)
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 300, 40), (9, 1000, 64), (40, 6144, 100), (70, 1600, 300), (200, 640, 90), (200, 2600, 90)])
+@pytest.mark.parametrize("g,u", [(-200.0, 2.0 ** 123), (-100.0, -2.0 ** 125), (-2.0 ** 100, 2.0 ** 100), (-1000.0, 2.0 ** 126)])
+def test_int8_mlp(T, H, I, g, u):
+    m, x = extreme_mlp(H, I, g, u)
+    x, xs = x.expand(T, H).contiguous(), torch.ones(T, device="cuda")
+    x = torch.nn.functional.pad(x, (0, -H % 16))[:, :H]
+    got = q4.mlp_i8(m, x, xs, dtype=F)
+    check_mlp(got, m, x.cpu(), xs.cpu())
