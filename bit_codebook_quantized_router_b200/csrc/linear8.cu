@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
     const float xs = a.xs[t];
     float y = scaled(v, xs, a.ws[n]);
     if (GATED)
-      y = silu_mul_fast(y, scaled(u, xs, a.ws[a.N + n]));
+      y = swiglu(y, scaled(u, xs, a.ws[a.N + n]));
     else if (a.bias)
       y += a.bias[n];
     store_out(a, t, n, y);

@@ -37,6 +37,17 @@ __device__ __forceinline__ float scaled(int acc, float xs, float ws) {
   return __fmul_rn((float)acc, __fmul_rn(xs, ws));
 }
 
+// silu(g) u, within 6 ulp of fp32 to g = -87 (below, e^g is subnormal, rounded
+// to 2^-149): e^-|g| does not overflow, so the denominator is in [1, 2], where
+// __fdividef is within 2 ulp.  Measured, MLP of 600 tokens, H = 2048, I = 1024,
+// and of 2048, H = 6144, I = 2048: 18.7 and 63.1 us; with an exact division
+// (silu_mul) 23.3 and 64.9; with silu_mul_fast 18.3 and 62.2, but its error grows
+// with |g| and it is 0 from g = -87.4 on, however large u is.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
+}
+
 __device__ __forceinline__ void store_out(const LinArgs& a, long long t, int n, float v) {
   if (a.out_f32)
     reinterpret_cast<float*>(a.out)[t * a.ldo + n] = v;

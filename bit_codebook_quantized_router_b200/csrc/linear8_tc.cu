@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads)
           const float xs = s_xs[c];
           float y = scaled(v[j], xs, wscale);
           if (GATED)
-            y = silu_mul_fast(y, scaled(u[j], xs, uscale));
+            y = swiglu(y, scaled(u[j], xs, uscale));
           else if (a.bias)
             y += bias;
           store_out(a, c_lo + c, n, y);
@@ -577,7 +577,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             split(mul(f2((float)(int)p[0], (float)(int)p[1]), mul(xs2, f2(g.x, g.y))), z[0], z[1]);
             split(mul(f2((float)(int)p[2], (float)(int)p[3]), mul(xs2, f2(g.z, g.w))), z[2], z[3]);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) y[j + h] = silu_mul_fast(y[j + h], z[h]);
+            for (int h = 0; h < 4; ++h) y[j + h] = swiglu(y[j + h], z[h]);
           } else if (a.bias) {
             const float4 b = *reinterpret_cast<const float4*>(sb + j);
             y[j] += b.x, y[j + 1] += b.y, y[j + 2] += b.z, y[j + 3] += b.w;

@@ -49,3 +49,14 @@ def test_int8_mlp(T, H, I, g, u):
     x = torch.nn.functional.pad(x, (0, -H % 16))[:, :H]
     got = q4.mlp_i8(m, x, xs, dtype=F)
     check_mlp(got, m, x.cpu(), xs.cpu())
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 300, 40), (9, 1000, 64), (40, 6144, 100), (70, 1600, 300), (200, 640, 90), (200, 2600, 90)])
+@pytest.mark.parametrize("g,u", [(-87.5, 2.0 ** 124), (-88.5, 2.0 ** 126), (-20.0, 2.0 ** 30), (-60.0, -2.0 ** 86)])
+def test_int8_mlp_small_sigmoids(T, H, I, g, u):
+    # silu(g) is small and u makes up for it: the channel is the row's largest,
+    # so its code is 127 in size and the row's scale is |h| / 127
+    m, x = extreme_mlp(H, I, g, u)
+    x = torch.nn.functional.pad(x.expand(T, H).contiguous(), (0, -H % 16))[:, :H]
+    xs = torch.ones(T, device="cuda")
+    check_mlp(q4.mlp_i8(m, x, xs, dtype=F), m, x.cpu(), xs.cpu())
