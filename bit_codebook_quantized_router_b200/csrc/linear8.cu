@@ -5,8 +5,8 @@
 //
 // The sums are taken in int32 and are exact: |x w| <= 2^14, so K up to
 // 131,071 cannot overflow, and they do not depend on the order or on how K is
-// split.  The one rounding of a sum is its conversion to fp32; the product of
-// the scales and the result's are one each, and the result's type is the last.
+// split.  The one rounding of a sum is its conversion to fp32; its products with
+// the two scales are one each, and the result's type is the last.
 #include "linear8.cuh"
 
 namespace q4 {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) f
       v += s_acc[(w * 8 * NT + t) * 16 + r];
       if (GATED) u += s_acc[(w * 8 * NT + t) * 16 + r + 8];
     }
-    const float xs = a.xs[t];
+    const RowFactor xs = row_factor(a.xs[t]);
     float y = scaled(v, xs, a.ws[n]);
     if (GATED)
       y = swiglu(y, scaled(u, xs, a.ws[a.N + n]));

@@ -30,11 +30,28 @@ struct LinArgs {
 #endif
 };
 
-// The one place that turns a sum into a value: the same bits in every kernel.
-// (__fmul_rn: a product that is not contracted with a bias behind it, as the
-// two-at-a-time products of wide_kernel are not)
-__device__ __forceinline__ float scaled(int acc, float xs, float ws) {
-  return __fmul_rn((float)acc, __fmul_rn(xs, ws));
+// What turns a sum into a value: (sum * x_scale) * w_scale, each product rounded
+// (__fmul_rn, and packed products in wide_kernel: none is contracted with a bias
+// behind it), the same bits in every kernel.  Not x_scale * w_scale first, which
+// leaves fp32's range where the result does not: the sum, below 2^31, is a whole
+// number, so its product with a small x_scale loses nothing that the result would
+// keep; one with an x_scale of 2^96 and more could overflow, so those are taken
+// down by 2^64 and the value brought up again, both exact.
+constexpr float kScaleBig = 0x1p96f, kScaleDown = 0x1p-64f, kScaleUp = 0x1p64f;
+
+struct RowFactor {
+  float s;   // x_scale, or x_scale * kScaleDown
+  bool up;   // the latter
+};
+
+__device__ __forceinline__ RowFactor row_factor(float xs) {
+  const bool up = fabsf(xs) >= kScaleBig;
+  return {up ? xs * kScaleDown : xs, up};
+}
+
+__device__ __forceinline__ float scaled(int acc, RowFactor x, float ws) {
+  const float v = __fmul_rn(__fmul_rn((float)acc, x.s), ws);
+  return x.up ? __fmul_rn(v, kScaleUp) : v;
 }
 
 // silu(g) u, within 6 ulp of fp32 to g = -87 (below, e^g is subnormal, rounded

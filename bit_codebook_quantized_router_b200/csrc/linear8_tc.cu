@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint64_t full[kMidStages], empty[kMidStages], acc_full[1], in_full[1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word, in_abort_word;
-  __shared__ float s_xs[kLinearMidTokens];
+  __shared__ RowFactor s_xs[kLinearMidTokens];
   volatile int* abort_flag = &abort_word;
   volatile int* in_abort = &in_abort_word;
   uint8_t* smem = align1024(smem_raw);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads)
       mbar_wait(acc_full, 0, abort_flag, wait_ns(a));
     }
   } else if (et < c_n) {
-    s_xs[et] = a.xs[c_lo + et];
+    s_xs[et] = row_factor(a.xs[c_lo + et]);
   }
   __syncthreads();
   // every MMA is done, or a wait was given up
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 4; ++j) {
           const int c = c0 + j * kStep;
           if (c >= c_n) break;
-          const float xs = s_xs[c];
+          const RowFactor xs = s_xs[c];
           float y = scaled(v[j], xs, wscale);
           if (GATED)
             y = swiglu(y, scaled(u[j], xs, uscale));
@@ -496,7 +496,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
         if (!GATED && e < BN) s_bias[buf * 256 + e] = a.bias && n < a.N ? a.bias[n] : 0.0f;
       }
       const long long t = (long long)m * 256 + rank * 128 + quad * 32 + lane;
-      const float xs = t < a.T ? a.xs[t] : 0.0f;
+      const RowFactor xf = row_factor(t < a.T ? a.xs[t] : 0.0f);
       named_bar(1, 32 * kEpiWarps);
       // (a warp whose wait was given up still meets the others at the barrier)
       if (lost || (lost = !mbar_wait_warp(&acc_full[buf], (use >> 1) & 1, abort_flag, wait_ns(a)))) continue;
@@ -561,21 +561,27 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
         const int c = part * kOwn + half * kCols + i * 16;
         const float* sc = s_scale + buf * 256 + c;
         const float* sb = s_bias + buf * 256 + c;
-        const F2 xs2 = f2(xs, xs);
+        const F2 xs2 = f2(xf.s, xf.s);
         float y[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           // (as scaled(), two at a time)
           const float4 w = *reinterpret_cast<const float4*>(sc + j);
           const uint32_t* q = v[i & 1] + j;
-          split(mul(f2((float)(int)q[0], (float)(int)q[1]), mul(xs2, f2(w.x, w.y))), y[j], y[j + 1]);
-          split(mul(f2((float)(int)q[2], (float)(int)q[3]), mul(xs2, f2(w.z, w.w))), y[j + 2], y[j + 3]);
+          split(mul(mul(f2((float)(int)q[0], (float)(int)q[1]), xs2), f2(w.x, w.y)), y[j], y[j + 1]);
+          split(mul(mul(f2((float)(int)q[2], (float)(int)q[3]), xs2), f2(w.z, w.w)), y[j + 2], y[j + 3]);
+          if (xf.up)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) y[j + h] = __fmul_rn(y[j + h], kScaleUp);
           if (GATED) {
             const float4 g = *reinterpret_cast<const float4*>(sc + kBN + j);
             const uint32_t* p = u[i & 1] + j;
             float z[4];
-            split(mul(f2((float)(int)p[0], (float)(int)p[1]), mul(xs2, f2(g.x, g.y))), z[0], z[1]);
-            split(mul(f2((float)(int)p[2], (float)(int)p[3]), mul(xs2, f2(g.z, g.w))), z[2], z[3]);
+            split(mul(mul(f2((float)(int)p[0], (float)(int)p[1]), xs2), f2(g.x, g.y)), z[0], z[1]);
+            split(mul(mul(f2((float)(int)p[2], (float)(int)p[3]), xs2), f2(g.z, g.w)), z[2], z[3]);
+            if (xf.up)
+#pragma unroll
+              for (int h = 0; h < 4; ++h) z[h] = __fmul_rn(z[h], kScaleUp);
 #pragma unroll
             for (int h = 0; h < 4; ++h) y[j + h] = swiglu(y[j + h], z[h]);
           } else if (a.bias) {

@@ -482,9 +482,10 @@ MOE_Q4_API int moe_q4_add_norm(const void* x, int x_type, long long ldx, const v
                                long long ldq, float* scale, void* stream);
 
 /* moe_q4_linear_i8 -- the product of int8 rows and an int8 weight matrix:
- *   out[t][n] = x_scale[t] * w_scale[n] * sum_k x[t][k] * w[n][k] (+ bias[n]),
- * sums exact in int32 (any int8 codes, -128 among them), the rest in fp32, the
- * result rounded to out's type.  Deterministic; a row's result does not depend
+ *   out[t][n] = (sum_k x[t][k] * w[n][k]) * x_scale[t] * w_scale[n] (+ bias[n]),
+ * sums exact in int32 (any int8 codes, -128 among them), the rest in fp32 in
+ * this order (no product overflows where the result does not), the result
+ * rounded to out's type.  Deterministic; a row's result does not depend
  * on the other rows of the call.
  *   x        device int8 [T][ldx];   x_scale  device fp32 [T];
  *   w        device int8 [N][ldw];   w_scale  device fp32 [N];

@@ -6,7 +6,8 @@ import torch
 
 import bit_codebook_quantized_router_b200 as q4
 from bit_codebook_quantized_router_b200 import _lib
-from tests.test_gpu_int8 import F, mlp_weights, rows
+from tests import int8_plain as plain
+from tests.test_gpu_int8 import BF, F, gen, int8_rows, mlp_weights, on_gpu, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,36 @@ def test_limits_do_not_count_the_kernel_in_front(T, N, K):
     torch.cuda.synchronize()
     assert status.item() == 0
     assert torch.equal(got, want) and torch.equal(got_mlp, want_mlp)
+
+
+@pytest.mark.parametrize("dtype,bias", [(F, False), (F, True), (BF, False)])
+@pytest.mark.parametrize("T,N,K", [(11, 100, 4096), (40, 200, 4096), (100, 130, 4000), (200, 300, 1000), (200, 130, 4000), (200, 60, 6000)])
+def test_scales_at_both_ends_of_fp32(T, N, K, dtype, bias):
+    # every pair of scales from 2^-149 to 2^127: the products by themselves leave
+    # fp32's range where the result does not
+    ends = torch.tensor([2.0 ** -149, 3e-44, 1e-40, 1.1e-38, 1e-25, 1e-16, 1e-3, 1.0, 1e7, 1e20, 2.0 ** 95 * 1.99, 2.0 ** 96, 1e30, 3e38],
+                        dtype=torch.float64).float()
+    x, _ = int8_rows(T, K, 1)
+    w, _ = int8_rows(N, K, 2)
+    w[::7] = 0
+    xs, ws = ends[torch.arange(T) % len(ends)], ends[torch.arange(N) % 13 + torch.arange(N) // 13 % 2]
+    b = torch.randn(N, generator=gen(3)) if bias else None
+    got = q4.linear_i8(on_gpu(x), xs.cuda(), on_gpu(w), ws.cuda(), bias=None if b is None else b.cuda(), dtype=dtype).cpu()
+    want, bound = plain.linear(x, xs, w, ws, b), plain.linear_bound(x, xs, w, ws, b, dtype)
+    # (the bound's 1e-38 is for results below fp32's normal range: there half a unit of 2^-149, or bf16's 2^-133, is lost)
+    bound = bound - 1e-38 + 2.0 ** -133
+    top = torch.finfo(dtype).max
+    inside, outside = want.abs() + bound <= top, want.abs() - bound > top
+    assert bool(((got.double() - want).abs() <= bound)[inside].all())
+    assert torch.equal(got.double()[outside], want[outside].sign() * float("inf"))
+    assert not torch.isnan(got).any() and inside.any() and outside.any()
+
+
+@pytest.mark.parametrize("T,H,I", [(5, 300, 70), (40, 6144, 100), (100, 1600, 70), (200, 640, 90), (200, 2600, 90), (200, 5200, 60)])
+@pytest.mark.parametrize("e", [100, -100])
+def test_mlp_with_the_scales_shifted_by_a_power_of_two(T, H, I, e):
+    m = mlp_weights(H, I, 4)
+    gu, gus, dn, ds = m.tensors
+    x, xs = q4.quant_rows(rows(T, H, 5, spread=False).cuda())
+    moved = q4.MlpI8(gu, gus * 2.0 ** -e, dn, ds)
+    assert torch.equal(q4.mlp_i8(moved, x, xs * 2.0 ** e, dtype=F), q4.mlp_i8(m, x, xs, dtype=F))
