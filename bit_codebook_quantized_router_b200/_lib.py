@@ -294,7 +294,7 @@ def forward_ex(layer: Layer, shared, x: torch.Tensor, logits: torch.Tensor, k: i
     xq and x_scale are x's int8 rows where the caller has them, as add_norm
     gives them, else the call makes them) or None."""
     T = x.shape[0]
-    ldq = _shared_rows(layer, shared, xq, x_scale, T)
+    ldq = _shared_rows(layer, shared, x, xq, x_scale)
     if out is None:
         out = torch.empty((T, layer.H), dtype=torch.bfloat16, device=x.device)
     own_ws = ws is None
@@ -334,7 +334,7 @@ def forward_gated(layer: Layer, shared, router_w: torch.Tensor, x: torch.Tensor,
     if router_w.dtype != torch.bfloat16 or tuple(router_w.shape) != (layer.E, layer.H):
         raise ValueError(f"router_w must be bf16 [{layer.E}, {layer.H}]")
     T = x.shape[0]
-    ldq = _shared_rows(layer, shared, xq, x_scale, T)
+    ldq = _shared_rows(layer, shared, x, xq, x_scale)
     if out is None:
         out = torch.empty((T, layer.H), dtype=torch.bfloat16, device=x.device)
     own_ws = ws is None
@@ -684,14 +684,20 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
     return out
 
 
-def _shared_rows(layer, shared, xq, x_scale, T):
-    """Row stride of the int8 rows given to a forward beside x (0 for none)."""
+def _shared_rows(layer, shared, x, xq, x_scale):
+    """Row stride of the int8 rows given to a forward beside x (0 for none); an
+    int8 shared expert, those rows, the layer and x are on one device."""
     if (xq is None) != (x_scale is None):
         raise ValueError("xq and x_scale go together")
+    if not isinstance(shared, MlpI8):
+        if xq is not None:
+            raise ValueError("xq and x_scale are read by an int8 shared expert (MlpI8)")
+        return 0
+    dev = x.get_device()
+    for t, what in ((shared.tensors[0], "the MLP's weights"), (layer.gate_w, "the layer's weights")):
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{what} (on {t.device}) and x (on {x.device}) must be on one CUDA device")
     if xq is None:
         return 0
-    if not isinstance(shared, MlpI8):
-        raise ValueError("xq and x_scale are read by an int8 shared expert (MlpI8)")
-    dev = xq.get_device()
-    _vector(x_scale, "x_scale", dev, T)
-    return _rows(xq, "xq", dev, T, layer.H, _INT8)
+    _vector(x_scale, "x_scale", dev, x.shape[0])
+    return _rows(xq, "xq", dev, x.shape[0], layer.H, _INT8)
