@@ -575,10 +575,10 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
              q: torch.Tensor | None = None, scale: torch.Tensor | None = None, bf16: bool = True,
              quant: bool = True, stream=None):
     """Residual addition, root-mean-square norm and the norm's rows in bf16 and
-    int8 in one pass: r = x + residual (in the residual's type), then
-    r * weight / sqrt(mean(r^2) + eps).  x and residual bf16 or fp32 [T, H],
-    weight bf16 or fp32 [H] or None (ones).  Returns (r or None without a
-    residual, out bf16 [T, H] or None with bf16=False, codes int8 [T, H] and
+    int8 in one pass: r = x + residual (the fp32 sum, rounded to the residual's
+    type), then r * weight / sqrt(mean(r^2) + eps).  x and residual bf16 or fp32
+    [T, H], weight bf16 or fp32 [H] or None (ones).  Returns (r or None without
+    a residual, out bf16 [T, H] or None with bf16=False, codes int8 [T, H] and
     scales fp32 [T] or None with quant=False).  residual_out may be residual
     itself (in place), out may be a bf16 x."""
     dev, T, H, ldx = _first(x, "x", _ROW_TYPE)

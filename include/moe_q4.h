@@ -456,7 +456,8 @@ MOE_Q4_API int moe_q4_quant_rows(const void* x, int x_type, long long ldx, int T
 
 /* moe_q4_add_norm -- the residual's addition, the root-mean-square norm and
  * the norm's rows in bf16 and in int8, in one pass:
- *   r = x + residual, rounded to the residual's type  (r = x without one);
+ *   r = x + residual in fp32, that rounded to the residual's type  (two
+ *       roundings for a bf16 residual; r = x without one);
  *   p = r * weight  (fp32);   f = 1 / sqrt(mean(r^2) + eps)  (fp32);
  *   residual_out = r;   out = bf16(p f);
  *   codes of the row p;   scale = max|p| f / 127.

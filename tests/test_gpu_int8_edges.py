@@ -100,3 +100,16 @@ def test_mlp_with_the_scales_shifted_by_a_power_of_two(T, H, I, e):
     x, xs = q4.quant_rows(rows(T, H, 5, spread=False).cuda())
     moved = q4.MlpI8(gu, gus * 2.0 ** -e, dn, ds)
     assert torch.equal(q4.mlp_i8(moved, x, xs * 2.0 ** e, dtype=F), q4.mlp_i8(m, x, xs, dtype=F))
+
+
+def test_residual_is_the_fp32_sum_rounded_to_its_type():
+    # sums next to a tie of bf16: 1 + 2^-8 + 2^-30 is 1 + 2^-8 in fp32, a tie
+    # that goes to 1, and 1 + 3 2^-8 - 2^-30 one that goes to 1 + 2^-6; rounded
+    # once to bf16 they would be 1 + 2^-7
+    x = torch.tensor([2.0 ** -8 + 2.0 ** -30, 3 * 2.0 ** -8 - 2.0 ** -30, 2.0 ** -8 + 2.0 ** -23, 0.5], dtype=torch.float64)
+    want = torch.tensor([1.0, 1 + 2.0 ** -6, 1 + 2.0 ** -7, 1.5])
+    for T, pad in ((1, 4), (3, 5), (300, 4)):
+        row = torch.cat([x.float(), torch.zeros(pad)]).repeat(T, 1).cuda()
+        res = torch.ones((T, 4 + pad), dtype=BF, device="cuda")
+        r = q4.add_norm(row, None, residual=res)[0]
+        assert torch.equal(r[:, :4].float().cpu(), want.expand(T, 4))
