@@ -673,8 +673,8 @@ def mlp_i8(mlp: MlpI8, x: torch.Tensor, x_scale: torch.Tensor, out: torch.Tensor
         out = _new((T, H), dtype, x, stream)
     if ws is None:
         ws = _new((max(mlp_i8_workspace(mlp, T), 256),), torch.uint8, x, stream)
-    elif ws.get_device() != dev or ws.dtype != torch.uint8:
-        raise ValueError(f"ws must be uint8 on cuda:{dev} (alloc_workspace)")
+    elif ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous uint8 on cuda:{dev} (alloc_workspace)")
     if mlp.tensors[0].get_device() != dev:
         raise ValueError(f"the MLP's weights must be on cuda:{dev}")
     _call("moe_q4_mlp_i8", dev, stream, lib().moe_q4_mlp_i8, mlp.ref, x.data_ptr(), ldx,

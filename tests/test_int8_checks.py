@@ -76,3 +76,11 @@ def test_parts_on_one_device_pass():
     x, xq, s = OnDevice((4, 64), torch.bfloat16, 1), OnDevice((4, 64), torch.int8, 1), OnDevice((4,), torch.float32, 1)
     assert _lib._shared_rows(layer_on(1), mlp_on(1), x, xq, s) == 64
     assert _lib._shared_rows(layer_on(1), mlp_on(1), x, None, None) == 0
+
+
+def test_mlp_refuses_a_workspace_that_repeats_its_bytes():
+    x, s, out = OnDevice((4, 64), torch.int8, 0), OnDevice((4,), torch.float32, 0), OnDevice((4, 64), torch.bfloat16, 0)
+    m = mlp_on(0)
+    ws = OnDevice((q4.mlp_i8_workspace(m, 4),), torch.uint8, 0, strides=(0,))
+    with pytest.raises(ValueError, match="contiguous"):
+        q4.mlp_i8(m, x, s, out=out, ws=ws)
