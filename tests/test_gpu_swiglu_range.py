@@ -5,7 +5,7 @@ import torch
 
 import bit_codebook_quantized_router_b200 as q4
 from bit_codebook_quantized_router_b200 import inputs
-from tests.test_gpu_int8 import BF, F, check_mlp, gen
+from tests.test_gpu_int8 import BF, F, check_mlp, gen, mlp_weights, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,20 @@ def test_int8_mlp_small_sigmoids(T, H, I, g, u):
     x = torch.nn.functional.pad(x.expand(T, H).contiguous(), (0, -H % 16))[:, :H]
     xs = torch.ones(T, device="cuda")
     check_mlp(q4.mlp_i8(m, x, xs, dtype=F), m, x.cpu(), xs.cpu())
+
+
+@pytest.mark.parametrize("T,H,I,size", [(3, 640, 300, 1.0), (40, 2304, 256, 30.0), (100, 1600, 300, 8.0), (700, 512, 1000, 1.0),
+                                        (700, 512, 1000, 40.0), (300, 2600, 200, 8.0)])
+def test_h_is_the_fp32_formula_rounded_to_bf16(T, H, I, size):
+    # every step of the definition in fp32 (sums exact), on gates of about `size`:
+    # the MLP's result has the same bits
+    m = mlp_weights(H, I, T)
+    gu, gus, dn, ds = m.tensors
+    gus = gus * size
+    m = q4.MlpI8(gu, gus, dn, ds)
+    x, xs = q4.quant_rows(rows(T, H, I, spread=False).cuda())
+    product = lambda a, sa, b, sb: (a.double() @ b.double().T).float() * sa[:, None] * sb  # noqa: E731
+    g, u = product(x, xs, gu, gus).chunk(2, 1)
+    h = (g / (1 + torch.exp(-g)) * u).to(BF)
+    q, s = q4.quant_rows(h)
+    assert torch.equal(q4.mlp_i8(m, x, xs, dtype=F), product(q, s, dn, ds))
