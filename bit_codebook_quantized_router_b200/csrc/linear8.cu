@@ -71,8 +71,8 @@ __device__ __forceinline__ uint4 load_weight16(const int8_t* row, int k, int K, 
 // operands of two MMAs once K is permuted the same way in the tokens' rows.
 // The loads of U segments are under way before the first product, and in a
 // chain the first ones before the kernel in front is done.
-// Measured, N = K = 6144 from memory: 1 token 7.8 us (4.8 TB/s with the launch),
-// 8 tokens 8.3, 16 tokens 9.7; the memory's bandwidth and the launch bound it.
+// Measured, N = K = 6144 from memory: 1 token 7.9 us (4.8 TB/s with the launch),
+// 8 tokens 8.4, 16 tokens 9.8; the memory's bandwidth and the launch bound it.
 // Three CTAs an SM (85 registers): with two, 384 CTAs take two turns (9.2 us).
 template <int NT, int U, bool GATED>
 __global__ void __launch_bounds__(256, NT <= 2 || (NT == 4 && U == 1) ? 3 : 1) few_kernel(const __grid_constant__ LinArgs a) {
@@ -207,9 +207,9 @@ int launch_few(const LinArgs& a, cudaStream_t s) {
 // and their time grows less with tokens): up to 16 tokens always; to 64 where
 // the tokens' rows, which every CTA reads, are short and the CTAs fit the card
 // at once (three an SM with one segment at a time or two up to 32 tokens, one
-// beyond).  Measured, us, few_kernel and mid_kernel: 32 tokens, N = K = 2048 3.7
+// beyond).  Measured, us, few_kernel and mid_kernel: 32 tokens, N = K = 2048 3.4
 // and 7.6; N = 6144, K = 512 3.9 and 5.2; N = K = 6144 13.8 and 12.1; 64 tokens,
-// N = K = 2048 5.8 and 7.6; N = 2048, K = 4096 9.6 and 7.9; N = 6144, K = 512
+// N = K = 2048 5.5 and 7.6; N = 2048, K = 4096 9.6 and 7.9; N = 6144, K = 512
 // 8.3 and 6.3.
 bool few_tokens(const LinArgs& a, bool gated) {
   if (a.T <= kFewTokens) return true;

@@ -8,8 +8,8 @@
 // The partial sums are int32, so adding them is exact in any order: each CTA
 // sends the columns that another owns to that CTA's shared memory, and each
 // finishes its own columns.  No workspace and one launch.  Measured, N = K =
-// 6144 from memory: 17 tokens 10.5 us, 64 tokens 12.4 (3.1 TB/s with the
-// launch), 128 tokens 16.4.  At 64 the weights arrive from 2.4 to 8.5-10 us of a
+// 6144 from memory: 17 tokens 10.5 us, 64 tokens 12.5 (3.1 TB/s with the
+// launch), 128 tokens 16.5.  At 64 the weights arrive from 2.4 to 8.5-10 us of a
 // CTA's life, the exchange and the last step take 3.  With the weights as the MMA's N = 256 and the tokens as
 // its M, 64 tokens took 22 us: twice the sums to exchange, by half the warps.
 //
@@ -731,7 +731,7 @@ int launch_wide(const LinArgs& a, cudaStream_t s) {
   // what 10 to 20 k-steps do.  Measured at 256 tokens, us, unsplit and split:
   // N = 2048 in tiles of 128 over two pairs, K = 2048 8.0 and 8.1, K = 2560 9.1
   // and 8.7, K = 4096 12.9 and 10.8; N = 6144 in tiles of 256, K = 2560 11.1 and
-  // 12.0, K = 4096 14.8 and 14.0 (N = 8192 15.0 and 15.1), K = 6144 19.5 and
+  // 12.0, K = 4096 14.8 and 14.0 (N = 8192 15.0 and 15.1), K = 6144 19.0 and
   // 16.5; N = 512 over two and four pairs, K = 3584 9.5 and 9.8, K = 5120 11.3
   // and 10.6, K = 8192 14.7 and 12.4.
   if (a.K >= 5120 && 8 * t256 <= sms * 5 / 6) return launch_wide<GATED, 256, 4>(a, s);

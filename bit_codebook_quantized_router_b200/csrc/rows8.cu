@@ -488,7 +488,8 @@ int launch(const RowArgs& a, bool vec, cudaStream_t s) {
   } else {
     // fp32 (twice the bytes a vector, so enough are under way): 8192 rows of
     // 6144 with an fp32 residual 113 us (6.7 TB/s) with two vectors a thread,
-    // 118 with four, 151 with one
+    // 118 with four, 151 with one.  Unaligned rows in number: four values a thread,
+    // 2000 rows of 2047 codes 8.3 us (one or two 12.4), 8000 of 601 9.8 (13.4)
     const int nv = units > 2048 || (!vec && many && units > 512) ? 4 : (units > 1024 || (many && units > 256) ? 2 : 1);
     const int threads = ((units + nv - 1) / nv + 31) / 32 * 32;
     if (vec && nv == 1)
