@@ -62,6 +62,33 @@ def test_int8_mlp_small_sigmoids(T, H, I, g, u):
     check_mlp(q4.mlp_i8(m, x, xs, dtype=F), m, x.cpu(), xs.cpu())
 
 
+def fp32_formula(m, x, xs):
+    """The MLP's definition step by step in fp32, sums exact."""
+    gu, gus, dn, ds = m.tensors
+    product = lambda a, sa, b, sb: (a.double() @ b.double().T).float() * sa[:, None] * sb  # noqa: E731
+    g, u = product(x, xs, gu, gus).chunk(2, 1)
+    q, s = q4.quant_rows((g / (1 + torch.exp(-g)) * u).to(BF))
+    return product(q, s, dn, ds)
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("g,u", [(6 * 2.0 ** -149, 2.0 ** 127), (1.7 * 2.0 ** -130, 2.0 ** 126), (torch.finfo(F).max, 2.0 ** -126), (1e30, 1e-20),
+                                 (-88.6, 2.0 ** 126), (-88.9, 2.0 ** 126), (0.0, 2.0 ** 127), (-2.0 ** -149, 2.0 ** 127)])
+def test_h_of_the_smallest_and_largest_gates(T, g, u):
+    # one channel alone, its sums 1, so that the scales are g and u
+    H, I = 2304, 64
+    q = torch.zeros((2 * I, H), dtype=torch.int8)
+    q[3, 0], q[I + 3, 0] = (-1 if g < 0 else 1), 1
+    s = torch.ones(2 * I)
+    s[3], s[I + 3] = abs(g), u
+    down = torch.randint(-127, 128, (H, I), generator=gen(1), dtype=torch.int8)
+    m = q4.MlpI8(q.cuda(), s.cuda(), down.cuda(), torch.ones(H, device="cuda"))
+    x = torch.ones((T, H), dtype=torch.int8, device="cuda")
+    xs = torch.ones(T, device="cuda")
+    got, want = q4.mlp_i8(m, x, xs, dtype=F), fp32_formula(m, x, xs)
+    assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
 @pytest.mark.parametrize("T,H,I,size", [(3, 640, 300, 1.0), (40, 2304, 256, 30.0), (100, 1600, 300, 8.0), (700, 512, 1000, 1.0),
                                         (700, 512, 1000, 40.0), (300, 2600, 200, 8.0)])
 def test_h_is_the_fp32_formula_rounded_to_bf16(T, H, I, size):
@@ -72,8 +99,4 @@ def test_h_is_the_fp32_formula_rounded_to_bf16(T, H, I, size):
     gus = gus * size
     m = q4.MlpI8(gu, gus, dn, ds)
     x, xs = q4.quant_rows(rows(T, H, I, spread=False).cuda())
-    product = lambda a, sa, b, sb: (a.double() @ b.double().T).float() * sa[:, None] * sb  # noqa: E731
-    g, u = product(x, xs, gu, gus).chunk(2, 1)
-    h = (g / (1 + torch.exp(-g)) * u).to(BF)
-    q, s = q4.quant_rows(h)
-    assert torch.equal(q4.mlp_i8(m, x, xs, dtype=F), product(q, s, dn, ds))
+    assert torch.equal(q4.mlp_i8(m, x, xs, dtype=F), fp32_formula(m, x, xs))
